@@ -58,6 +58,7 @@ typedef enum kvq_status {
 typedef enum kvq_dtype {
   KVQ_F16 = 0,
   KVQ_BF16 = 1,
+  KVQ_FP8 = 2, /* e4m3 codes, a power-of-two scale for each block and kv head */
   KVQ_INT4 = 4,
   KVQ_INT8 = 8
 } kvq_dtype;
@@ -76,12 +77,16 @@ typedef enum kvq_dtype {
  * One layer's KV pool (KVPool of "pymllm Runtime Design"; shape from LMDeploy
  * article §2.2). slot = block_id * 16 + offset is the pool's kv index.
  *  k, v   : [num_blocks, 16, kv_heads, row] where row is head_dim 16-bit
- *           elements (F16/BF16), head_dim bytes (INT8 codes) or head_dim / 2
- *           bytes (INT4, two codes per byte, even index in the low nibble).
- *  k_sz, v_sz : INT8/INT4 only, else NULL. Pairs of fp16 (scale, zero), scale
+ *           elements (F16/BF16), head_dim bytes (INT8 and FP8 codes) or
+ *           head_dim / 2 bytes (INT4, two codes per byte, even index in the
+ *           low nibble).
+ *  k_sz, v_sz : F16/BF16: NULL. INT8/INT4: pairs of fp16 (scale, zero), scale
  *           first, laid out [num_blocks, kv_heads, 16]: the 16 pairs of one
  *           (block, head) are contiguous. A code c stands for c * scale + zero
  *           (LMDeploy article §2.4: per-head, per-token asymmetric).
+ *           FP8: bytes [num_blocks, kv_heads]; an e4m3 code c of a block whose
+ *           byte is e stands for c * 2^(e - 127), and for 0 where e is 0. A
+ *           pool starts with these bytes at zero; 255 is not a scale.
  */
 typedef struct kvq_pool {
   void* k;
@@ -113,6 +118,20 @@ typedef struct kvq_pool {
  *    and all codes are 0 when scale is 0 or not finite or zero not finite.
  *  Inputs must be finite; bf16 inputs beyond the fp16 range are outside the
  *  contract (their scale/zero saturate). Tokens that share a slot race.
+ *  For FP8 pools a block (of one kv head, of K or of V) fills under one scale.
+ *  A run is a maximal stretch of tokens that follow one another in
+ *  slot_mapping, in one block, with rising slots. With amax the largest finite
+ *  |x| of the run's rows and e the block's scale byte, taken as 0 where the run
+ *  writes the block's first row (which starts the block anew: its other rows
+ *  hold nothing until they are written):
+ *    e' = max(e, the smallest byte with amax <= 448 * 2^(e' - 127)),
+ *    code_i = x_i * 2^(127 - e') rounded to the nearest e4m3, ties to even
+ *    (beyond 448, and infinities: 448; NaN: NaN), and where e' > e the
+ *    block's other rows are rounded to e': code = code * 2^(e - e') (0 where e
+ *    was 0).
+ *  Runs of the same block in one call race (a request's new tokens are one run
+ *  in each block); so do two calls that store to one block at the same time.
+ *  bf16 inputs may have any finite value. At most 32767 kv heads.
  *  Returns KVQ_OK, KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED or KVQ_ERR_CUDA.
  */
 kvq_status kv_store_quant(const kvq_pool* pool, const void* k_new, const void* v_new,
@@ -218,6 +237,41 @@ kvq_status paged_decode_attn(const kvq_pool* pool, const void* q, int32_t q_dtyp
                              void* stream);
 
 /*
+ * What a score goes through between sm_scale * q . k and the softmax, in this
+ * order. Position p is that of the query, t of the token.
+ *  softcap      : 0 for none, else 1e-6 to 1e6: s = softcap * tanh(s / softcap).
+ *  alibi_slopes : NULL, or device float [q_heads]: s -= slope[h] * |p - t|.
+ *  prefix_lens  : NULL, or device int32 [batch]: the tokens t < prefix_lens[b]
+ *                 of request b are seen by its queries before them too (a
+ *                 prefix mask: both ways inside the prefix, causal behind it);
+ *                 clamped to the request's length. A decode's query is its
+ *                 request's last token, so it has no effect there.
+ *  window       : 0 for none, else only tokens t > p - window are seen (the
+ *                 query itself and window - 1 before it), the prefix's
+ *                 included. Blocks wholly before it are not read.
+ */
+typedef struct kvq_score {
+  float softcap;
+  int32_t window;
+  const float* alibi_slopes;
+  const int32_t* prefix_lens;
+} kvq_score;
+
+/*
+ * paged_decode_attn_scored -- paged_decode_attn with `score` (a host pointer,
+ * read during the call) applied to the scores; for pools of every kind. The
+ * pages have no counterpart: layers that cap, bias or window their scores read
+ * the same cache. Same plan and workspace as paged_decode_attn. Rows of the
+ * last block behind the request's last token are not used, whatever they hold.
+ */
+kvq_status paged_decode_attn_scored(const kvq_pool* pool, const kvq_score* score, const void* q,
+                                    int32_t q_dtype, void* out, const int32_t* block_tables,
+                                    int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                    int32_t batch, int32_t q_heads, int32_t max_seq_len,
+                                    float sm_scale, int32_t num_splits, void* workspace,
+                                    size_t workspace_bytes, int32_t* dev_err, void* stream);
+
+/*
  * paged_decode_attn_shared_prefix -- the same attention as paged_decode_attn,
  * computed as a cascade for requests that share leading blocks
  * ("pymllm Runtime Design", section "KV cache 与 prefix cache": radix prefix
@@ -247,7 +301,7 @@ kvq_status paged_decode_attn(const kvq_pool* pool, const void* q, int32_t q_dtyp
  * the shared part, a shared count above max_shared_blocks) sets
  * KVQ_DEV_ERR_PREFIX; the output rows of that group are then unspecified,
  * and no memory outside the arguments is touched. The result equals
- * paged_decode_attn's up to rounding order.
+ * paged_decode_attn's up to rounding order. FP8 pools: KVQ_ERR_UNSUPPORTED.
  */
 kvq_status paged_decode_attn_shared_prefix_workspace_size(
     int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_seq_len,
@@ -351,6 +405,20 @@ kvq_status paged_extend_attn(const kvq_pool* pool, const void* q, int32_t q_dtyp
                              size_t workspace_bytes, int32_t* dev_err, void* stream);
 
 /*
+ * paged_extend_attn_scored -- paged_extend_attn with `score` (a host pointer,
+ * read during the call) applied to the scores; for pools of every kind. Same
+ * workspace as paged_extend_attn. Query i of request b then sees
+ *   (t <= p or t < prefix_lens[b]) and t > p - window, of its kv_lens[b] tokens.
+ */
+kvq_status paged_extend_attn_scored(const kvq_pool* pool, const kvq_score* score, const void* q,
+                                    int32_t q_dtype, void* out, const int32_t* qo_indptr,
+                                    const int32_t* kv_lens, const int32_t* block_tables,
+                                    int32_t max_blocks_per_seq, int32_t batch, int32_t total_q,
+                                    int32_t q_heads, int32_t max_kv_len, float sm_scale,
+                                    int32_t variant, void* workspace, size_t workspace_bytes,
+                                    int32_t* dev_err, void* stream);
+
+/*
  * kvq_decode_step -- one decode step of a layer in a single launch: the
  * block tables from the ReqToTokenPool rows (as
  * kvq_block_tables_from_req_to_token), the quantizing store of the step's new
@@ -368,7 +436,8 @@ kvq_status paged_extend_attn(const kvq_pool* pool, const void* q, int32_t q_dtyp
  * request (kvq_decode_step_fused): its first phase runs at the attention's
  * occupancy, which suits a decode batch's new tokens but not a prefill chunk
  * stored in the same step (LMDeploy article §2.3, chunked prefill beside the
- * decodes); with more tokens the same work runs as four kernels.
+ * decodes); with more tokens, and for FP8 pools, the same work runs as four
+ * kernels.
  */
 int32_t kvq_decode_step_fused(int32_t batch, int64_t num_tokens);
 
@@ -412,7 +481,7 @@ kvq_status kvq_selftest_step_barrier(uint32_t* counter, int32_t grid_ctas, int32
  *  src_ids, dst_ids : int32 [n], device-addressable.
  * For every i, block src_ids[i] of src is copied to block dst_ids[i] of dst:
  * its K and V tiles (16 x kv_heads rows each) and, for INT8/INT4 pools, its
- * K and V (scale, zero) pairs. The dst ids must be distinct and, when src and
+ * K and V (scale, zero) pairs, for FP8 pools its scale bytes. The dst ids must be distinct and, when src and
  * dst are the same pool, none of them may also be a src id (the pairs run in
  * parallel). A pair with an id outside its pool is skipped and flagged
  * KVQ_DEV_ERR_BLOCK_ID. Asynchronous on `stream`; allocates nothing.

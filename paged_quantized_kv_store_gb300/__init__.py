@@ -23,8 +23,9 @@ from . import _build
 
 LIB_PATH = _build.LIB_PATH
 
-KVQ_F16, KVQ_BF16, KVQ_INT4, KVQ_INT8 = 0, 1, 4, 8
-DTYPE_CODES = {"f16": KVQ_F16, "bf16": KVQ_BF16, "int4": KVQ_INT4, "int8": KVQ_INT8}
+KVQ_F16, KVQ_BF16, KVQ_FP8, KVQ_INT4, KVQ_INT8 = 0, 1, 2, 4, 8
+DTYPE_CODES = {"f16": KVQ_F16, "bf16": KVQ_BF16, "fp8": KVQ_FP8, "int4": KVQ_INT4,
+               "int8": KVQ_INT8}
 BLOCK_SIZE = 16
 HEAD_DIM = 128
 
@@ -52,6 +53,11 @@ class _Pool(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("kv_dtype", ctypes.c_int32)]
 
 
+class _Score(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("alibi_slopes", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p)]
+
+
 class _Plan(ctypes.Structure):
     _fields_ = [("min_blocks_per_warp", ctypes.c_int32), ("warps", ctypes.c_int32),
                 ("head_groups", ctypes.c_int32), ("heads_per_group", ctypes.c_int32),
@@ -64,7 +70,8 @@ EXPORTED = ["kv_store_quant", "kvq_block_tables_from_req_to_token", "paged_decod
             "kvq_status_string", "kvq_version", "paged_decode_attn_noalloc",
             "paged_decode_attn_shared_prefix_workspace_size", "paged_decode_attn_shared_prefix",
             "kvq_copy_blocks", "paged_extend_attn_workspace_size", "paged_extend_attn",
-            "kvq_decode_step_workspace_size", "kvq_decode_step", "kvq_decode_step_fused"]
+            "kvq_decode_step_workspace_size", "kvq_decode_step", "kvq_decode_step_fused",
+            "paged_decode_attn_scored", "paged_extend_attn_scored"]
 
 
 def load(build_if_missing: bool = False):
@@ -92,6 +99,14 @@ def load(build_if_missing: bool = False):
     lib.paged_decode_attn.argtypes = [ctypes.POINTER(_Pool), P, I32, P, P, I32, P, I32, I32, I32,
                                       F, I32, P, SZ, P, P]
     lib.paged_decode_attn.restype = ctypes.c_int
+    lib.paged_decode_attn_scored.argtypes = [ctypes.POINTER(_Pool), ctypes.POINTER(_Score), P,
+                                             I32, P, P, I32, P, I32, I32, I32, F, I32, P, SZ, P,
+                                             P]
+    lib.paged_decode_attn_scored.restype = ctypes.c_int
+    lib.paged_extend_attn_scored.argtypes = [ctypes.POINTER(_Pool), ctypes.POINTER(_Score), P,
+                                             I32, P, P, P, P, I32, I32, I32, I32, I32, F, I32, P,
+                                             SZ, P, P]
+    lib.paged_extend_attn_scored.restype = ctypes.c_int
     lib.paged_decode_attn_noalloc.argtypes = [ctypes.POINTER(_Pool), P, I32, P, P, I32, P, I32,
                                               I32, I32, F, I32, P, P]
     lib.paged_decode_attn_noalloc.restype = ctypes.c_int
@@ -152,9 +167,11 @@ class KVPool:
     """One layer's KV pool on the device (KVPool of "pymllm Runtime Design").
 
     k, v: uint8/int16 tensors [num_blocks, 16, kv_heads, row] where row is
-    head_dim 16-bit elements (f16/bf16), head_dim bytes (int8) or head_dim/2
-    bytes (int4); k_sz, v_sz: int32 [num_blocks, kv_heads, 16] holding fp16
-    (scale, zero) pairs, or None for f16/bf16 pools.
+    head_dim 16-bit elements (f16/bf16), head_dim bytes (int8, and e4m3 codes
+    of fp8) or head_dim/2 bytes (int4); k_sz, v_sz: int32 [num_blocks,
+    kv_heads, 16] holding fp16 (scale, zero) pairs for int8/int4, uint8
+    [num_blocks, kv_heads] holding a power-of-two scale e (2^(e - 127), 0 for
+    zeros) for fp8, or None for f16/bf16 pools.
     """
 
     k: object
@@ -174,7 +191,7 @@ class KVPool:
         (the swap target of kvq_copy_blocks)."""
         import torch
         row = {"f16": 2 * head_dim, "bf16": 2 * head_dim, "int8": head_dim,
-               "int4": head_dim // 2}[kv_dtype]
+               "fp8": head_dim, "int4": head_dim // 2}[kv_dtype]
         shape = (num_blocks, BLOCK_SIZE, kv_heads, row)
         kw = dict(device="cpu", pin_memory=True) if pinned else dict(device=device)
         k = torch.zeros(shape, dtype=torch.uint8, **kw)
@@ -183,6 +200,9 @@ class KVPool:
             szs = (num_blocks, kv_heads, BLOCK_SIZE)
             k_sz = torch.zeros(szs, dtype=torch.int32, **kw)
             v_sz = torch.zeros(szs, dtype=torch.int32, **kw)
+        elif kv_dtype == "fp8":
+            k_sz = torch.zeros((num_blocks, kv_heads), dtype=torch.uint8, **kw)
+            v_sz = torch.zeros((num_blocks, kv_heads), dtype=torch.uint8, **kw)
         else:
             k_sz = v_sz = None
         return KVPool(k, v, k_sz, v_sz, num_blocks, kv_heads, kv_dtype, head_dim)
@@ -195,7 +215,7 @@ class KVPool:
     def nbytes(self) -> int:
         n = self.k.numel() + self.v.numel()
         if self.k_sz is not None:
-            n += 4 * (self.k_sz.numel() + self.v_sz.numel())
+            n += self.k_sz.element_size() * (self.k_sz.numel() + self.v_sz.numel())
         return n
 
 
@@ -258,6 +278,45 @@ def paged_decode_attn(pool: KVPool, q, out, block_tables, seq_lens, max_seq_len,
                                float(sm_scale), int(num_splits), _ptr(workspace), ws_bytes,
                                _ptr(dev_err), _stream(stream))
     _check(st, "paged_decode_attn")
+
+
+@dataclass
+class Score:
+    """What a score goes through before the softmax (kvq_score of kvq.h):
+    softcap (0: none), window in tokens (0: none), alibi_slopes (float32
+    [q_heads] on the device, or None) and prefix_lens (int32 [batch] on the
+    device, or None)."""
+
+    softcap: float = 0.0
+    window: int = 0
+    alibi_slopes: object = None
+    prefix_lens: object = None
+
+    def c_struct(self, q_heads: int, batch: int) -> _Score:
+        import torch
+        for name, t, dt, n in (("alibi_slopes", self.alibi_slopes, torch.float32, q_heads),
+                               ("prefix_lens", self.prefix_lens, torch.int32, batch)):
+            if t is not None and (t.dtype != dt or t.numel() != n or not t.is_contiguous()):
+                raise ValueError(f"Score.{name}: expected {n} contiguous values of {dt}, got "
+                                 f"{tuple(t.shape)} of {t.dtype}")
+        return _Score(float(self.softcap), int(self.window), _ptr(self.alibi_slopes),
+                      _ptr(self.prefix_lens))
+
+
+def paged_decode_attn_scored(pool: KVPool, score: Score, q, out, block_tables, seq_lens,
+                             max_seq_len, sm_scale, num_splits=0, workspace=None, dev_err=None,
+                             stream=None):
+    """paged_decode_attn with capped, biased or windowed scores; see kvq.h."""
+    lib = load()
+    ps = pool.c_struct()
+    sc = score.c_struct(int(q.shape[1]), int(q.shape[0]))
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib.paged_decode_attn_scored(
+        ctypes.byref(ps), ctypes.byref(sc), _ptr(q), _dtype_code(q), _ptr(out),
+        _ptr(block_tables), int(block_tables.shape[1]), _ptr(seq_lens), int(q.shape[0]),
+        int(q.shape[1]), int(max_seq_len), float(sm_scale), int(num_splits), _ptr(workspace),
+        ws_bytes, _ptr(dev_err), _stream(stream))
+    _check(st, "paged_decode_attn_scored")
 
 
 def paged_decode_attn_noalloc(pool: KVPool, q, out, block_tables, seq_lens, max_seq_len,
@@ -437,6 +496,23 @@ def paged_extend_attn(pool: KVPool, q, out, qo_indptr, kv_lens, block_tables, ma
                                float(sm_scale), EXTEND_VARIANTS[variant], _ptr(workspace),
                                ws_bytes, _ptr(dev_err), _stream(stream))
     _check(st, "paged_extend_attn")
+
+
+def paged_extend_attn_scored(pool: KVPool, score: Score, q, out, qo_indptr, kv_lens,
+                             block_tables, max_kv_len, sm_scale, workspace=None, dev_err=None,
+                             stream=None, variant="auto"):
+    """paged_extend_attn with capped or biased scores, a window or a prefix
+    mask; see kvq.h."""
+    lib = load()
+    ps = pool.c_struct()
+    sc = score.c_struct(int(q.shape[1]), int(kv_lens.numel()))
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib.paged_extend_attn_scored(
+        ctypes.byref(ps), ctypes.byref(sc), _ptr(q), _dtype_code(q), _ptr(out), _ptr(qo_indptr),
+        _ptr(kv_lens), _ptr(block_tables), int(block_tables.shape[1]), int(kv_lens.numel()),
+        int(q.shape[0]), int(q.shape[1]), int(max_kv_len), float(sm_scale),
+        EXTEND_VARIANTS[variant], _ptr(workspace), ws_bytes, _ptr(dev_err), _stream(stream))
+    _check(st, "paged_extend_attn_scored")
 
 
 def kvq_copy_blocks(src: KVPool, dst: KVPool, src_ids, dst_ids, dev_err=None, stream=None):

@@ -19,6 +19,7 @@ using kvq::kHeadDim;
 namespace {
 
 constexpr int kAutoMinBlocksPerWarp = 4;  // a warp's range is never shorter than this
+constexpr float kMinSoftcap = 1e-6f, kMaxSoftcap = 1e6f;
 
 // Decode workspace: [256 bytes: the tail-chunk counter, the fused step's
 // barrier counter][header: 4 ints + batch + 1 prefix sums][partial records:
@@ -39,14 +40,17 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 bool is_quant(int dt) { return dt == KVQ_INT8 || dt == KVQ_INT4; }
 bool is_float16(int dt) { return dt == KVQ_F16 || dt == KVQ_BF16; }
+bool is_fp8(int dt) { return dt == KVQ_FP8; }
 
 kvq_status check_pool(const kvq_pool* p) {
   if (p == nullptr || p->k == nullptr || p->v == nullptr) return KVQ_ERR_INVALID_ARG;
   if (p->num_blocks < 0 || p->kv_heads <= 0) return KVQ_ERR_INVALID_ARG;
   if (p->block_size != kBlock || p->head_dim != kHeadDim) return KVQ_ERR_UNSUPPORTED;
-  if (!is_quant(p->kv_dtype) && !is_float16(p->kv_dtype)) return KVQ_ERR_UNSUPPORTED;
+  if (!is_quant(p->kv_dtype) && !is_float16(p->kv_dtype) && !is_fp8(p->kv_dtype))
+    return KVQ_ERR_UNSUPPORTED;
+  if (is_fp8(p->kv_dtype) && p->kv_heads > kvq::kMaxFp8Heads) return KVQ_ERR_UNSUPPORTED;
   if (!aligned16(p->k) || !aligned16(p->v)) return KVQ_ERR_INVALID_ARG;
-  if (is_quant(p->kv_dtype)) {
+  if (is_quant(p->kv_dtype) || is_fp8(p->kv_dtype)) {
     if (p->k_sz == nullptr || p->v_sz == nullptr) return KVQ_ERR_INVALID_ARG;
     if (!aligned16(p->k_sz) || !aligned16(p->v_sz)) return KVQ_ERR_INVALID_ARG;
   }
@@ -131,6 +135,27 @@ bool encode_pool_map_heads(CUtensorMap* map, void* base, int64_t num_blocks, int
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+kvq_status check_score(const kvq_score* s) {
+  if (s == nullptr) return KVQ_ERR_INVALID_ARG;
+  if (!std::isfinite(s->softcap) || s->softcap < 0.f || s->window < 0) return KVQ_ERR_INVALID_ARG;
+  if (s->softcap > 0.f && (s->softcap < kMinSoftcap || s->softcap > kMaxSoftcap))
+    return KVQ_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(s->alibi_slopes) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(s->prefix_lens) & 3u) != 0)
+    return KVQ_ERR_INVALID_ARG;
+  return KVQ_OK;
+}
+
+kvq::ScoreArgs score_args(const kvq_score& s) {
+  kvq::ScoreArgs a;
+  a.cap = s.softcap * 1.4426950408889634f;
+  a.cap_in = s.softcap > 0.f ? 0.6931471805599453f / s.softcap : 0.f;
+  a.window = s.window;
+  a.slopes = s.alibi_slopes;
+  a.prefix_lens = s.prefix_lens;
+  return a;
+}
+
 // Shared-prefix groups as the caller describes them.
 struct PrefixDesc {
   const int32_t* offsets;
@@ -181,9 +206,12 @@ kvq_status decode_impl(const kvq_pool* pool, const void* q, int32_t q_dtype, voi
                        const int32_t* seq_lens, int32_t batch, int32_t q_heads,
                        int32_t max_seq_len, float sm_scale, int32_t num_splits,
                        const PrefixDesc* pd, void* workspace, size_t workspace_bytes,
-                       int32_t* dev_err, void* stream, const StepPre* pre = nullptr) {
+                       int32_t* dev_err, void* stream, const StepPre* pre = nullptr,
+                       const kvq_score* score = nullptr) {
   const kvq_status ps = check_pool(pool);
   if (ps != KVQ_OK) return ps;
+  const bool fp8 = is_fp8(pool->kv_dtype);
+  if (fp8 && pd != nullptr) return KVQ_ERR_UNSUPPORTED;  // the cascade has no FP8 form
   if (!is_float16(q_dtype)) return KVQ_ERR_UNSUPPORTED;
   if (is_float16(pool->kv_dtype) && q_dtype != pool->kv_dtype) return KVQ_ERR_UNSUPPORTED;
   if (batch < 0 || q_heads <= 0 || max_blocks_per_seq <= 0 || max_seq_len < 0)
@@ -213,7 +241,10 @@ kvq_status decode_impl(const kvq_pool* pool, const void* q, int32_t q_dtype, voi
   std::memset(&a, 0, sizeof(a));
   // the grouped-query kernel (INT8 / INT4 pools, fp16 queries, 4 q heads per
   // kv head) serves the plain decode; the fused step keeps the general kernel
-  const bool gqa = pre == nullptr && kvq::decode_gqa_supported(pool->kv_dtype, q_dtype,
+  // the kernels with scores and those over FP8 pools are their own
+  const bool scored = score != nullptr && (score->softcap > 0.f || score->window > 0 ||
+                                           score->alibi_slopes != nullptr);
+  const bool gqa = pre == nullptr && !scored && kvq::decode_gqa_supported(pool->kv_dtype, q_dtype,
                                                                 q_heads / pool->kv_heads,
                                                                 pool->kv_heads);
   const int cta_heads = gqa ? kvq::decode_gqa_cta_heads(pool->kv_heads) : 0;
@@ -226,7 +257,7 @@ kvq_status decode_impl(const kvq_pool* pool, const void* q, int32_t q_dtype, voi
       return KVQ_ERR_CUDA;
   }
   // the general INT8 kernels (decode, shared prefix, step) stage one tile per copy
-  if (pool->kv_dtype == KVQ_INT8) {
+  if (pool->kv_dtype == KVQ_INT8 || fp8) {
     if (!encode_pool_map(&a.k_map, pool->k, pool->num_blocks, pool->kv_heads, kHeadDim) ||
         !encode_pool_map(&a.v_map, pool->v, pool->num_blocks, pool->kv_heads, kHeadDim))
       return KVQ_ERR_CUDA;
@@ -238,6 +269,9 @@ kvq_status decode_impl(const kvq_pool* pool, const void* q, int32_t q_dtype, voi
   a.v = static_cast<const uint8_t*>(pool->v);
   a.k_sz = static_cast<const uint32_t*>(pool->k_sz);
   a.v_sz = static_cast<const uint32_t*>(pool->v_sz);
+  a.k_se = static_cast<const uint8_t*>(pool->k_sz);
+  a.v_se = static_cast<const uint8_t*>(pool->v_sz);
+  if (scored) a.score = score_args(*score);
   a.num_blocks = pool->num_blocks;
   a.kv_heads = pool->kv_heads;
   a.q = q;
@@ -331,6 +365,14 @@ kvq_status decode_impl(const kvq_pool* pool, const void* q, int32_t q_dtype, voi
   if (gqa) {
     if (kvq::launch_decode_gqa(a, pool->kv_dtype, gqa_grid, s) != cudaSuccess)
       return KVQ_ERR_CUDA;
+  } else if (fp8 || scored) {
+    const int per_sm = std::min(
+        kvq::decode_scored_ctas_per_sm(pool->kv_dtype, q_dtype, scored, batch),
+        kvq::kMaxCtasPerSm);
+    if (per_sm <= 0) return KVQ_ERR_CUDA;
+    if (kvq::launch_decode_scored(a, pool->kv_dtype, q_dtype, scored, plan.num_sms * per_sm, s) !=
+        cudaSuccess)
+      return KVQ_ERR_CUDA;
   } else {
     const int per_sm = std::min(kvq::decode_ctas_per_sm(pool->kv_dtype, q_dtype, batch, tail),
                                 kvq::kMaxCtasPerSm);
@@ -382,7 +424,7 @@ ExtendPlan extend_plan(int batch, int total_q, int q_heads, int kv_heads, int ma
 
 extern "C" {
 
-int32_t kvq_version(void) { return 101; }
+int32_t kvq_version(void) { return 102; }
 
 const char* kvq_status_string(kvq_status s) {
   switch (s) {
@@ -424,6 +466,10 @@ kvq_status kv_store_quant(const kvq_pool* pool, const void* k_new, const void* v
   a.slot_mapping = slot_mapping;
   a.num_tokens = num_tokens;
   a.dev_err = dev_err;
+  if (is_fp8(pool->kv_dtype))
+    return kvq::launch_store_fp8(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KVQ_OK
+               : KVQ_ERR_CUDA;
   return kvq::launch_store(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK
                                                                                   : KVQ_ERR_CUDA;
 }
@@ -493,6 +539,19 @@ kvq_status paged_decode_attn(const kvq_pool* pool, const void* q, int32_t q_dtyp
                      workspace_bytes, dev_err, stream);
 }
 
+kvq_status paged_decode_attn_scored(const kvq_pool* pool, const kvq_score* score, const void* q,
+                                    int32_t q_dtype, void* out, const int32_t* block_tables,
+                                    int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                    int32_t batch, int32_t q_heads, int32_t max_seq_len,
+                                    float sm_scale, int32_t num_splits, void* workspace,
+                                    size_t workspace_bytes, int32_t* dev_err, void* stream) {
+  const kvq_status st = check_score(score);
+  if (st != KVQ_OK) return st;
+  return decode_impl(pool, q, q_dtype, out, block_tables, max_blocks_per_seq, seq_lens, batch,
+                     q_heads, max_seq_len, sm_scale, num_splits, nullptr, workspace,
+                     workspace_bytes, dev_err, stream, nullptr, score);
+}
+
 kvq_status paged_decode_attn_shared_prefix_workspace_size(
     int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_seq_len,
     int32_t num_splits, int32_t max_shared_blocks, size_t* bytes) {
@@ -543,12 +602,13 @@ kvq_status paged_extend_attn_workspace_size(int32_t batch, int32_t total_q, int3
   return KVQ_OK;
 }
 
-kvq_status paged_extend_attn(const kvq_pool* pool, const void* q, int32_t q_dtype, void* out,
-                             const int32_t* qo_indptr, const int32_t* kv_lens,
-                             const int32_t* block_tables, int32_t max_blocks_per_seq,
-                             int32_t batch, int32_t total_q, int32_t q_heads, int32_t max_kv_len,
-                             float sm_scale, int32_t variant, void* workspace,
-                             size_t workspace_bytes, int32_t* dev_err, void* stream) {
+static kvq_status extend_impl(const kvq_pool* pool, const kvq_score* score, const void* q,
+                              int32_t q_dtype, void* out, const int32_t* qo_indptr,
+                              const int32_t* kv_lens, const int32_t* block_tables,
+                              int32_t max_blocks_per_seq, int32_t batch, int32_t total_q,
+                              int32_t q_heads, int32_t max_kv_len, float sm_scale,
+                              int32_t variant, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_err, void* stream) {
   const kvq_status ps = check_pool(pool);
   if (ps != KVQ_OK) return ps;
   if (!is_float16(q_dtype)) return KVQ_ERR_UNSUPPORTED;
@@ -560,7 +620,11 @@ kvq_status paged_extend_attn(const kvq_pool* pool, const void* q, int32_t q_dtyp
   if (variant < KVQ_EXTEND_AUTO || variant > KVQ_EXTEND_TCGEN05) return KVQ_ERR_INVALID_ARG;
   // the tcgen05 kernel reads a missing block's rows from block 0 (and masks
   // them), so it needs a pool with at least one block
-  const bool tc_ok = kvq::extend_tc_supported(pool->kv_dtype, q_dtype) &&
+  const bool fp8 = is_fp8(pool->kv_dtype);
+  const bool scored = score != nullptr &&
+                      (score->softcap > 0.f || score->window > 0 ||
+                       score->alibi_slopes != nullptr || score->prefix_lens != nullptr);
+  const bool tc_ok = !scored && kvq::extend_tc_supported(pool->kv_dtype, q_dtype) &&
                      batch <= kvq::extend_tc_max_batch() && pool->num_blocks > 0;
   if (variant == KVQ_EXTEND_TCGEN05 && !tc_ok) return KVQ_ERR_UNSUPPORTED;
   if (batch > kvq::kMaxBatch) return KVQ_ERR_UNSUPPORTED;
@@ -576,11 +640,14 @@ kvq_status paged_extend_attn(const kvq_pool* pool, const void* q, int32_t q_dtyp
   if (workspace == nullptr || workspace_bytes < plan.total) return KVQ_ERR_WORKSPACE;
   kvq::ExtendArgs a;
   std::memset(&a, 0, sizeof(a));
-  if (pool->kv_dtype == KVQ_INT8) {
+  if (pool->kv_dtype == KVQ_INT8 || fp8) {
     if (!encode_pool_map(&a.k_map, pool->k, pool->num_blocks, pool->kv_heads, kHeadDim) ||
         !encode_pool_map(&a.v_map, pool->v, pool->num_blocks, pool->kv_heads, kHeadDim))
       return KVQ_ERR_CUDA;
   }
+  a.k_se = static_cast<const uint8_t*>(pool->k_sz);
+  a.v_se = static_cast<const uint8_t*>(pool->v_sz);
+  if (scored) a.score = score_args(*score);
   a.k = static_cast<const uint8_t*>(pool->k);
   a.v = static_cast<const uint8_t*>(pool->v);
   a.k_sz = static_cast<const uint32_t*>(pool->k_sz);
@@ -621,11 +688,44 @@ kvq_status paged_extend_attn(const kvq_pool* pool, const void* q, int32_t q_dtyp
                ? KVQ_OK
                : KVQ_ERR_CUDA;
   }
+  if (fp8 || scored) {
+    const int n = kvq::extend_scored_ctas_per_sm(pool->kv_dtype, q_dtype, scored, batch);
+    if (n <= 0) return KVQ_ERR_CUDA;
+    return kvq::launch_extend_scored(a, pool->kv_dtype, q_dtype, scored, sms * n, s) ==
+                   cudaSuccess
+               ? KVQ_OK
+               : KVQ_ERR_CUDA;
+  }
   const int per_sm = kvq::extend_ctas_per_sm(pool->kv_dtype, q_dtype, batch);
   if (per_sm <= 0) return KVQ_ERR_CUDA;
   return kvq::launch_extend(a, pool->kv_dtype, q_dtype, sms * per_sm, s) == cudaSuccess
              ? KVQ_OK
              : KVQ_ERR_CUDA;
+}
+
+kvq_status paged_extend_attn(const kvq_pool* pool, const void* q, int32_t q_dtype, void* out,
+                             const int32_t* qo_indptr, const int32_t* kv_lens,
+                             const int32_t* block_tables, int32_t max_blocks_per_seq,
+                             int32_t batch, int32_t total_q, int32_t q_heads, int32_t max_kv_len,
+                             float sm_scale, int32_t variant, void* workspace,
+                             size_t workspace_bytes, int32_t* dev_err, void* stream) {
+  return extend_impl(pool, nullptr, q, q_dtype, out, qo_indptr, kv_lens, block_tables,
+                     max_blocks_per_seq, batch, total_q, q_heads, max_kv_len, sm_scale, variant,
+                     workspace, workspace_bytes, dev_err, stream);
+}
+
+kvq_status paged_extend_attn_scored(const kvq_pool* pool, const kvq_score* score, const void* q,
+                                    int32_t q_dtype, void* out, const int32_t* qo_indptr,
+                                    const int32_t* kv_lens, const int32_t* block_tables,
+                                    int32_t max_blocks_per_seq, int32_t batch, int32_t total_q,
+                                    int32_t q_heads, int32_t max_kv_len, float sm_scale,
+                                    int32_t variant, void* workspace, size_t workspace_bytes,
+                                    int32_t* dev_err, void* stream) {
+  const kvq_status st = check_score(score);
+  if (st != KVQ_OK) return st;
+  return extend_impl(pool, score, q, q_dtype, out, qo_indptr, kv_lens, block_tables,
+                     max_blocks_per_seq, batch, total_q, q_heads, max_kv_len, sm_scale, variant,
+                     workspace, workspace_bytes, dev_err, stream);
 }
 
 kvq_status kvq_decode_step_workspace_size(int32_t batch, int32_t q_heads, int32_t kv_heads,
@@ -682,9 +782,10 @@ kvq_status kvq_decode_step(const kvq_pool* pool, const int32_t* req_to_token,
   if (batch < 0) return KVQ_ERR_INVALID_ARG;
   if (batch == 0)  // nothing to attend: the step is the store alone
     return kv_store_quant(pool, k_new, v_new, q_dtype, slot_mapping, num_tokens, dev_err, stream);
-  if (!kvq_decode_step_fused(batch, num_tokens)) {
+  if (!kvq_decode_step_fused(batch, num_tokens) || is_fp8(pool->kv_dtype)) {
     // a prefill chunk rides along: its store runs at full occupancy in a
-    // kernel of its own, and so do the tables and the attention
+    // kernel of its own, and so do the tables and the attention; and the FP8
+    // store joins a run's rows in a CTA, which the one launch has no phase for
     kvq_status st = kvq_block_tables_from_req_to_token(
         req_to_token, num_req_slots, max_context_len, req_pool_indices, seq_lens, batch,
         max_blocks_per_seq, block_tables, dev_err, stream);
@@ -726,8 +827,9 @@ kvq_status kvq_copy_blocks(const kvq_pool* src, const kvq_pool* dst, const int32
   if (n < 0) return KVQ_ERR_INVALID_ARG;
   if (n == 0) return KVQ_OK;
   if (src_ids == nullptr || dst_ids == nullptr) return KVQ_ERR_INVALID_ARG;
-  const int row = is_quant(src->kv_dtype) ? (src->kv_dtype == KVQ_INT8 ? kHeadDim : kHeadDim / 2)
-                                          : 2 * kHeadDim;
+  const int row = src->kv_dtype == KVQ_INT4                              ? kHeadDim / 2
+                  : src->kv_dtype == KVQ_INT8 || is_fp8(src->kv_dtype) ? kHeadDim
+                                                                       : 2 * kHeadDim;
   kvq::CopyArgs a;
   a.src_k = static_cast<const uint4*>(src->k);
   a.src_v = static_cast<const uint4*>(src->v);
@@ -740,6 +842,7 @@ kvq_status kvq_copy_blocks(const kvq_pool* src, const kvq_pool* dst, const int32
   a.src_blocks = src->num_blocks;
   a.dst_blocks = dst->num_blocks;
   a.tile_chunks = static_cast<int64_t>(kBlock) * src->kv_heads * row / 16;
+  a.se_bytes = is_fp8(src->kv_dtype) ? src->kv_heads : 0;
   a.sz_chunks = is_quant(src->kv_dtype) ? static_cast<int64_t>(src->kv_heads) * kBlock * 4 / 16 : 0;
   a.src_ids = src_ids;
   a.dst_ids = dst_ids;

@@ -6,7 +6,8 @@
 // same copy forks a shared block before a request writes into it. A block is
 // four contiguous runs in the pool layout: its K tile and V tile (16 rows x
 // kv_heads x row bytes each) and, for quantized pools, its K and V
-// (scale, zero) runs (kv_heads x 16 x 4 bytes each). Either pool may sit in
+// (scale, zero) runs (kv_heads x 16 x 4 bytes each), or, for FP8 pools, its
+// scale bytes (kv_heads each). Either pool may sit in
 // pinned host memory that the GPU addresses directly (unified addressing):
 // the kernel then reads or writes host memory over the CPU-GPU link.
 //
@@ -66,6 +67,15 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs a) {
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u)
     if (dst[u] != nullptr) __stcs(dst[u], v[u]);
+  if (blockIdx.y == 0) {  // FP8 pools: the block's scale bytes
+    const int64_t n = a.se_bytes;
+    for (int64_t e = threadIdx.x; e < 2 * n; e += kCopyThreads) {
+      const bool is_v = e >= n;
+      const int64_t i = is_v ? e - n : e;
+      reinterpret_cast<uint8_t*>(is_v ? a.dst_v_sz : a.dst_k_sz)[d * n + i] =
+          reinterpret_cast<const uint8_t*>(is_v ? a.src_v_sz : a.src_k_sz)[s * n + i];
+    }
+  }
 }
 
 }  // namespace

@@ -16,12 +16,23 @@ namespace kvq {
 // CTA's dynamic shared memory, warp_sum 4 ints of static shared memory.
 // TAIL: the instantiation that can hand out tail chunks (make_range_map);
 // without it a warp has one range, as the tail-free sizes want.
-template <int KV, bool QBF, bool TAIL>
+// SC: scores go through a.score (a cap, a distance bias, a window) before the
+// softmax; the token positions below count from the first block read, which
+// leaves distances to the query, the request's last token, as they are.
+// FP8 pools (kvq_fp8.cuh): the codes enter both products as exact fp16. A
+// block's K scale multiplies its scores. Its V scale goes into the weights as
+// a power of two relative to the request's reference exponent (vref): while
+// the block's lies within [-2, 10] of it the weights stay normal fp16 numbers,
+// else the output so far is rescaled to the block's; the output takes the
+// reference once, at the end.
+template <int KV, bool QBF, bool TAIL, bool SC = false>
 __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* dsmem,
                                             int32_t* warp_sum, int cta, int ncta) {
   using S = Stage<KV>;
   constexpr bool kQuant = KvTraits<KV>::kQuant;
   constexpr bool kPvBf = KV == kBF16;  // P.V product type: bf16 only for bf16 pools
+  constexpr bool kF8Pool = KV == kF8;
+  constexpr bool kQkBf = QBF && !kF8Pool;  // Q.K product type: FP8 pools take fp16 always
   constexpr float kAk = CodeOffset<KV, QBF>::kK;
   constexpr float kAv = CodeOffset<KV, QBF>::kV;
   constexpr float kMid = CodeOffset<KV, QBF>::kMid;
@@ -33,7 +44,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
 
   // ---- blocks per request, prefix-summed (every CTA); the cut into ranges ------
   constexpr bool kLockstep = KV != kI4;
-  const StreamPlan sp = plan_stream<QBF, TAIL>(a, dsmem, warp_sum, cta, ncta, kLockstep);
+  const StreamPlan sp = plan_stream<QBF, TAIL, SC>(a, dsmem, warp_sum, cta, ncta, kLockstep);
   const int32_t* cum = sp.cum;
   unsigned char* stages = sp.stages;
   const int tb = sp.tb;
@@ -65,8 +76,11 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
     Cursor ic;
     locate(ic, x0, cum, a.batch, tb);
     Cursor cc = ic;  // compute side
-    int win_b = -1, win_j0 = 0;
+    int win_b = -1, win_j0 = 0, win_hgi = -1;
     int32_t win = -1;
+    // FP8 pools: K and V scale bytes of the window's blocks, one per lane, and
+    // of the blocks in flight (stage s in lane s)
+    uint32_t win_se = 0u, ring_se = 0u;
     uint32_t ok_mask = 0;  // stages holding a valid block in flight
     int k_issue = 0;   // next block of the range to issue
     int st_issue = 0;  // its stage
@@ -74,17 +88,30 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
       if (k_issue < n) {
         // (a range that crosses into the next q-head group of a lone request
         // starts over at its first block)
-        if (ic.b != win_b || ic.j < win_j0 || ic.j >= win_j0 + 32) {
+        if (ic.b != win_b || ic.j < win_j0 || ic.j >= win_j0 + 32 ||
+            (kF8Pool && ic.hgi != win_hgi)) {
           win_b = ic.b;
           win_j0 = ic.j;
           const int jj = win_j0 + lane;
           win = jj < ic.nblk ? a.block_tables[static_cast<int64_t>(ic.b) * a.max_blocks +
-                                              skip_of(a, ic.b) + jj]
+                                              lead_of<SC>(a, ic.b) + jj]
                              : -1;
+          if constexpr (kF8Pool) {
+            win_hgi = ic.hgi;
+            win_se = 0u;
+            if (win >= 0 && win < a.num_blocks) {
+              const int64_t e = static_cast<int64_t>(win) * a.kv_heads + ic.hgi / a.head_groups;
+              win_se = a.k_se[e] | static_cast<uint32_t>(a.v_se[e]) << 8;
+            }
+          }
         }
         const int32_t phys = __shfl_sync(kFull, win, ic.j - win_j0);
         const bool ok = phys >= 0 && phys < a.num_blocks;
         const uint32_t bit = 1u << st_issue;
+        if constexpr (kF8Pool) {
+          const uint32_t se = __shfl_sync(kFull, win_se, ic.j - win_j0);
+          if (lane == st_issue) ring_se = se;
+        }
         if (ok) {
           issue_block<KV>(wr, st_issue, a, lm, phys, ic.hgi / a.head_groups, lane);
           ok_mask |= bit;
@@ -107,6 +134,10 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
     uint32_t qb[8][2];
     float qs0 = 0.f, qs1 = 0.f;  // sum(q) of heads 2t and 2t+1
     bool hv0 = false, hv1 = false;
+    uint32_t vref = 0u;           // FP8 pools: scale byte o is counted in (0: none yet)
+    float qd0 = 1.f, qd1 = 1.f;   // FP8 pools, bf16 queries: factors of heads 2t, 2t + 1
+    float sl0 = 0.f, sl1 = 0.f;   // distance bias of those heads, times log2(e)
+    int wlo = 0;                  // first token inside the window
     float o[8][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, z0 = 0.f, z1 = 0.f;
     float r0 = 0.f, r1 = 0.f;  // sums of the 16-bit P' values fed to the P.V product
@@ -131,6 +162,13 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
         // o = sum P'(a + c) + sum p (Z + mid S) - (a + mid) sum P'
         z0 -= (kAv + kMid) * r0;
         z1 -= (kAv + kMid) * r1;
+      }
+      if constexpr (kF8Pool) {
+        const float unit = fp8_scale(vref);
+  #pragma unroll
+        for (int i = 0; i < 8; ++i)
+  #pragma unroll
+          for (int c = 0; c < 4; ++c) o[i][c] *= unit;
       }
       const bool contained = seg_start >= x0 && seg_start + seg_nblk <= x0 + n;
       const int64_t row0 = static_cast<int64_t>(seg_b) * a.q_heads + hq0;
@@ -205,8 +243,9 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
         const int hg = cc.hgi - h * a.head_groups;
         hq0 = h * a.group + hg * kHeadsPerGroup;
         nh = min(kHeadsPerGroup, a.group - hg * kHeadsPerGroup);
-        seg_skip = skip_of(a, cc.b);
-        L = clamped_len(a, cc.b) - kBlock * seg_skip;  // tokens of this request's own blocks
+        seg_skip = SC ? 0 : skip_of(a, cc.b);
+        // tokens of this request's own blocks
+        L = clamped_len(a, cc.b) - kBlock * lead_of<SC>(a, cc.b);
         // Q fragments (B operand of S^T = K Q^T), permuted like the K dims
         uint32_t qw[16];
         if (g < nh) {
@@ -221,6 +260,11 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
         } else {
   #pragma unroll
           for (int i = 0; i < 16; ++i) qw[i] = 0u;
+        }
+        if constexpr (kF8Pool && QBF) {
+          const float down = q_to_f16(qw);  // lanes 4h hold head h
+          qd0 = __shfl_sync(kFull, down, (2 * t) * 4);
+          qd1 = __shfl_sync(kFull, down, (2 * t + 1) * 4);
         }
         if constexpr (KV == kI4) {
   #pragma unroll
@@ -247,6 +291,14 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
         }
         hv0 = 2 * t < nh;
         hv1 = 2 * t + 1 < nh;
+        if constexpr (SC) {
+          wlo = a.score.window > 0 ? max(L - a.score.window, 0) : 0;
+          if (a.score.slopes != nullptr) {
+            sl0 = hv0 ? a.score.slopes[hq0 + 2 * t] * 1.4426950408889634f : 0.f;
+            sl1 = hv1 ? a.score.slopes[hq0 + 2 * t + 1] * 1.4426950408889634f : 0.f;
+          }
+        }
+        vref = 0u;
   #pragma unroll
         for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         m0 = m1 = -INFINITY;
@@ -257,15 +309,30 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
         ok_mask &= ~(1u << st);
         Frag<KV> cur;
         read_frag<KV>(cur, wr, st, lm, g);
+        uint32_t ke = 0u, ve = 0u;  // FP8 pools: the block's scale bytes
+        if constexpr (kF8Pool) {
+          const uint32_t se = __shfl_sync(kFull, ring_se, st);
+          ke = se & 0xFFu;
+          ve = se >> 8;
+          if (ve == 0u) clear_v_rows<KV>(cur, t, 0, 0);
+        }
+        if constexpr (kF8Pool || SC) {
+          const int left = L - cc.j * kBlock, skip = wlo - cc.j * kBlock;
+          if (left < kBlock || skip > 0) clear_v_rows<KV>(cur, t, skip, left);
+          if constexpr (kQuant) {  // ... and the scale/zero words of those tokens
+            if (g >= left || g < skip) cur.vsz[0] = 0u;
+            if (g + 8 >= left || g + 8 < skip) cur.vsz[1] = 0u;
+          }
+        }
         // S^T = K Q^T, even and odd k-steps in two accumulators
         float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
   #pragma unroll
         for (int kk = 0; kk < 8; kk += 2) {
           uint32_t ak[4];
           k_operand<KV, QBF>(cur, kk, ak);
-          mma16816<QBF>(sa, ak, qb[kk]);
+          mma16816<kQkBf>(sa, ak, qb[kk]);
           k_operand<KV, QBF>(cur, kk + 1, ak);
-          mma16816<QBF>(sb, ak, qb[kk + 1]);
+          mma16816<kQkBf>(sb, ak, qb[kk + 1]);
         }
         const float sc0 = sa[0] + sb[0], sc1 = sa[1] + sb[1];
         const float sc2 = sa[2] + sb[2], sc3 = sa[3] + sb[3];
@@ -280,11 +347,35 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
           s01 = (S0 * sc1 + Z0 * qs1) * a.sm_scale_log2;
           s10 = (S1 * sc2 + Z1 * qs0) * a.sm_scale_log2;
           s11 = (S1 * sc3 + Z1 * qs1) * a.sm_scale_log2;
+        } else if constexpr (kF8Pool) {
+          const float f = fp8_scale(ke) * a.sm_scale_log2;
+          const float f0 = QBF ? f * qd0 : f, f1 = QBF ? f * qd1 : f;
+          s00 = ke != 0u ? sc0 * f0 : 0.f;
+          s01 = ke != 0u ? sc1 * f1 : 0.f;
+          s10 = ke != 0u ? sc2 * f0 : 0.f;
+          s11 = ke != 0u ? sc3 * f1 : 0.f;
         } else {
           s00 = sc0 * a.sm_scale_log2;
           s01 = sc1 * a.sm_scale_log2;
           s10 = sc2 * a.sm_scale_log2;
           s11 = sc3 * a.sm_scale_log2;
+        }
+        if constexpr (SC) {
+          if (a.score.cap > 0.f) {
+            s00 = softcap(a.score, s00);
+            s01 = softcap(a.score, s01);
+            s10 = softcap(a.score, s10);
+            s11 = softcap(a.score, s11);
+          }
+          if (a.score.slopes != nullptr) {
+            const float d0 = static_cast<float>(L - 1 - tok0), d1 = d0 - 8.f;
+            s00 -= sl0 * d0;
+            s01 -= sl1 * d0;
+            s10 -= sl0 * d1;
+            s11 -= sl1 * d1;
+          }
+          if (tok0 < wlo) s00 = s01 = -INFINITY;
+          if (tok1 < wlo) s10 = s11 = -INFINITY;
         }
         if (tok0 >= L) s00 = s01 = -INFINITY;
         if (tok1 >= L) s10 = s11 = -INFINITY;
@@ -333,6 +424,27 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
           z0 += p00 * Z0 + p10 * Z1;
           z1 += p01 * Z0 + p11 * Z1;
           q00 *= S0; q01 *= S0; q10 *= S1; q11 *= S1;
+        }
+        if constexpr (kF8Pool) {
+          if (ve != 0u) {
+            int d = static_cast<int>(ve) - static_cast<int>(vref);
+            if (vref == 0u) {  // nothing but blocks of zeros so far
+              vref = ve;
+              d = 0;
+            } else if (d > 10 || (d < -2 && d >= -90)) {
+              // 2^-d; blocks 2^90 below the reference only lose what is lost
+              // in the output's own rounding
+              const float by = d > 126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 - d) << 23);
+  #pragma unroll
+              for (int i = 0; i < 8; ++i)
+  #pragma unroll
+                for (int c = 0; c < 4; ++c) o[i][c] *= by;
+              vref = ve;
+              d = 0;
+            }
+            const float f = d < -90 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + d) << 23);
+            q00 *= f; q01 *= f; q10 *= f; q11 *= f;
+          }
         }
         // P'^T as the B operand: transpose the (token x head) fragments
         uint32_t bp[2], bp_lo[2];

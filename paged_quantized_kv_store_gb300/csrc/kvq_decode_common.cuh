@@ -38,9 +38,21 @@ __device__ __forceinline__ int skip_of(const DecodeArgs& a, int b) {
   return a.skip != nullptr ? a.skip[b] : 0;
 }
 
+// Leading blocks of request b this kernel does not read: the shared ones, or
+// (SC, a scored decode) those that lie wholly before the window.
+template <bool SC>
+__device__ __forceinline__ int lead_of(const DecodeArgs& a, int b) {
+  if constexpr (SC) {
+    return a.score.window > 0 ? max(clamped_len(a, b) - a.score.window, 0) / kBlock : 0;
+  } else {
+    return skip_of(a, b);
+  }
+}
+
 // Blocks of request b this kernel reads.
+template <bool SC = false>
 __device__ __forceinline__ int own_blocks(const DecodeArgs& a, int b) {
-  return max((clamped_len(a, b) + kBlock - 1) / kBlock - skip_of(a, b), 0);
+  return max((clamped_len(a, b) + kBlock - 1) / kBlock - lead_of<SC>(a, b), 0);
 }
 
 // Merges the shared-prefix records of (request, q head) `row` into a state
@@ -128,7 +140,7 @@ struct StreamPlan {
 // whose only blocks are shared ones is written by the combine kernel).
 // The CTA has blockDim.x threads (at most 8 warps: warp_sum holds one int per
 // warp) and owns ranges_per_cta ranges of the stream (one per warp, or one).
-template <bool QBF, bool TAIL>
+template <bool QBF, bool TAIL, bool SC = false>
 __device__ __forceinline__ StreamPlan plan_stream(const DecodeArgs& a, unsigned char* dsmem,
                                                   int32_t* warp_sum, int cta, int ncta,
                                                   bool lockstep, bool own_lens = false,
@@ -142,7 +154,7 @@ __device__ __forceinline__ StreamPlan plan_stream(const DecodeArgs& a, unsigned 
     const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
     int sum = 0;
     for (int b = b0; b < b1; ++b) {
-      sum += own_blocks(a, b);
+      sum += own_blocks<SC>(a, b);
       if (cta == 0 && a.seq_lens[b] > a.len_cap) report(a.dev_err, KVQ_DEV_ERR_LENGTH);
     }
     int incl = sum;
@@ -158,8 +170,8 @@ __device__ __forceinline__ StreamPlan plan_stream(const DecodeArgs& a, unsigned 
     int run = base + incl - sum;
     for (int b = b0; b < b1; ++b) {
       cum[b] = run;
-      run += own_blocks(a, b);
-      if (own_lens) lown[b] = clamped_len(a, b) - kBlock * skip_of(a, b);
+      run += own_blocks<SC>(a, b);
+      if (own_lens) lown[b] = clamped_len(a, b) - kBlock * lead_of<SC>(a, b);
     }
     if (tid == nt - 1) cum[a.batch] = base + incl;
     __syncthreads();

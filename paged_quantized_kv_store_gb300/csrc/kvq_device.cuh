@@ -11,8 +11,15 @@
 namespace kvq {
 
 // element kinds as template tags
-enum Kind : int { kF16 = KVQ_F16, kBF16 = KVQ_BF16, kI4 = KVQ_INT4, kI8 = KVQ_INT8 };
+enum Kind : int {
+  kF16 = KVQ_F16,
+  kBF16 = KVQ_BF16,
+  kF8 = KVQ_FP8,
+  kI4 = KVQ_INT4,
+  kI8 = KVQ_INT8
+};
 
+// kQuant: codes with a (scale, zero) for each token and head
 template <int KV>
 struct KvTraits;
 template <>
@@ -23,6 +30,11 @@ struct KvTraits<kF16> {
 template <>
 struct KvTraits<kBF16> {
   static constexpr int kRowBytes = 2 * kHeadDim;
+  static constexpr bool kQuant = false;
+};
+template <>
+struct KvTraits<kF8> {  // e4m3 codes, one scale for each block and head (kvq_fp8.cuh)
+  static constexpr int kRowBytes = kHeadDim;
   static constexpr bool kQuant = false;
 };
 template <>

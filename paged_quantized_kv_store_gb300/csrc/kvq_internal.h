@@ -42,6 +42,16 @@ struct TablesArgs {
   int32_t* dev_err;
 };
 
+// Score forms of the scored attention: what a score goes through between the
+// product and the softmax, in the exp2 domain.
+struct ScoreArgs {
+  float cap;       // softcap * log2(e); 0: none
+  float cap_in;    // ln(2) / softcap: a score over the cap
+  int window;      // 0: none
+  const float* slopes;         // [q_heads], or null
+  const int32_t* prefix_lens;  // [batch], or null
+};
+
 struct DecodeArgs {
   // TMA descriptors of the K and V pools (quantized pools only): 4-D views
   // [num_blocks][16][kv_heads][row bytes], one box = one (block, head) tile
@@ -98,6 +108,10 @@ struct DecodeArgs {
   // one-tile view the other INT8 kernels use)
   CUtensorMap kh_map;
   CUtensorMap vh_map;
+  // FP8 pools: the scale bytes [num_blocks][kv_heads]
+  const uint8_t* k_se;
+  const uint8_t* v_se;
+  ScoreArgs score;  // scored kernels only
 };
 
 struct CopyArgs {
@@ -113,6 +127,7 @@ struct CopyArgs {
   int64_t dst_blocks;
   int64_t tile_chunks;  // 16-byte chunks of one block's K (or V) tile
   int64_t sz_chunks;    // 16-byte chunks of one block's K (or V) scale/zero run
+  int se_bytes;         // FP8 pools: scale bytes of one block's K (or V); else 0
   const int32_t* src_ids;
   const int32_t* dst_ids;
   int32_t* dev_err;
@@ -144,6 +159,9 @@ struct ExtendArgs {
   int32_t* counter;            // work counter (zero at launch)
   float* part;                 // [total_q][Hq][max_splits][kPartStride] when split
   int32_t* dev_err;
+  const uint8_t* k_se;         // FP8 pools: the scale bytes [num_blocks][kv_heads]
+  const uint8_t* v_se;
+  ScoreArgs score;             // scored kernels only
 };
 
 // One decode step in a single cooperative launch: block tables, the store of
@@ -156,6 +174,7 @@ struct StepArgs {
 };
 
 cudaError_t launch_store(const StoreArgs& a, cudaStream_t s);
+cudaError_t launch_store_fp8(const StoreArgs& a, cudaStream_t s);
 // kv_dtype / q_dtype as for launch_decode (the new rows have Q's dtype)
 cudaError_t launch_step(const StepArgs& a, int kv_dtype, int q_dtype, int grid_ctas,
                         cudaStream_t s);
@@ -166,6 +185,11 @@ cudaError_t launch_barrier_selftest(unsigned int* ctr, int32_t* dev_err, int gri
 cudaError_t launch_extend(const ExtendArgs& a, int kv_dtype, int q_dtype, int grid_ctas,
                           cudaStream_t s);
 int extend_ctas_per_sm(int kv_dtype, int q_dtype, int batch);
+// the same over FP8 pools, and with scores over pools of any kind
+// (kvq_extend_scored.cu)
+cudaError_t launch_extend_scored(const ExtendArgs& a, int kv_dtype, int q_dtype, bool scored,
+                                 int grid_ctas, cudaStream_t s);
+int extend_scored_ctas_per_sm(int kv_dtype, int q_dtype, bool scored, int batch);
 // the tcgen05 version (256-row units; INT8, INT4 and fp16 pools)
 bool extend_tc_supported(int kv_dtype, int q_dtype);
 cudaError_t launch_extend_tc(const ExtendArgs& a, int kv_dtype, int q_dtype, int grid_ctas,
@@ -180,6 +204,12 @@ cudaError_t launch_decode(const DecodeArgs& a, int kv_dtype, int q_dtype, int gr
 cudaError_t launch_combine(const DecodeArgs& a, int q_dtype, cudaStream_t s);
 cudaError_t launch_prefix(const DecodeArgs& a, int kv_dtype, int q_dtype, int grid_ctas,
                           cudaStream_t s);
+
+// The decode over FP8 pools, and the scored decode over pools of any kind
+// (kvq_decode_scored.cu): same workspace and combine.
+cudaError_t launch_decode_scored(const DecodeArgs& a, int kv_dtype, int q_dtype, bool scored,
+                                 int grid_ctas, cudaStream_t s);
+int decode_scored_ctas_per_sm(int kv_dtype, int q_dtype, bool scored, int batch);
 
 // CTAs of the decode kernel resident per SM (occupancy) for a dtype pair and batch
 int decode_ctas_per_sm(int kv_dtype, int q_dtype, int batch, bool tail);
@@ -197,6 +227,7 @@ int prefix_ctas_per_sm(int kv_dtype, int q_dtype, int num_groups);
 
 constexpr int kMaxBatch = 8192;        // request lengths are scanned in shared memory
 constexpr uint32_t kMaxStoreRows = 0xFFFFFFFFu;  // store rows (tokens x 2 x kv heads) per call
+constexpr int kMaxFp8Heads = 32767;    // kv heads of an FP8 pool: a grid dimension of its store
 constexpr int kDecodeThreads = 128;
 constexpr int kMaxCtasPerSm = 4;       // the workspace has slots for this many CTAs per SM
 constexpr int kPartStride = kHeadDim + 4;  // floats per partial record (16-byte multiple)

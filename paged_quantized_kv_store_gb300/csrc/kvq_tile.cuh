@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "kvq_device.cuh"
+#include "kvq_fp8.cuh"
 #include "kvq_internal.h"
 
 namespace kvq {
@@ -41,6 +42,8 @@ struct Frag<kI8> {
   uint4 v[4];      // 16 bytes: dims [16g, 16g+16)
   uint32_t ksz[2], vsz[2];
 };
+template <>
+struct Frag<kF8> : Frag<kI8> {};
 template <>
 struct Frag<kI4> {
   uint4 k[2];      // 16 bytes: dims [32t, 32t+32)
@@ -78,17 +81,18 @@ struct Stage {
   // TMA for INT8 tiles (2 KB boxes); INT4 tiles (1 KB) stream faster through
   // per-lane cp.async (measured on the same GPU: 57 vs 64 us for the INT4
   // GQA-4 workload)
-  static constexpr bool kTma = KV == kI8;
+  static constexpr bool kTma = KV == kI8 || KV == kF8;
   static constexpr int kCopies = kBlock * kChunks / 32;    // cp.async chunks per lane per tile
   static constexpr int kKReads = kChunks / 4;              // 16-byte K reads per row
   static constexpr int kVReads = kChunks >= 8 ? kChunks / 8 : 1;  // V reads per row
   // blocks in flight per warp (about 8-16 KB of KV per warp)
-  static constexpr int kDepth = KV == kI4 ? 4 : (KV == kI8 ? 4 : 2);
+  static constexpr int kDepth = KV == kI4 ? 4 : (kTma ? 4 : 2);
   static constexpr int kVOff = kDepth * kTile;
   static constexpr int kSzOff = 2 * kDepth * kTile;
   static constexpr int kBarOff = kSzOff + kDepth * 128;
   static constexpr int kWarpBytes = (kBarOff + kDepth * 8 + 1023) / 1024 * 1024;
-  static constexpr int kTxBytes = kTma ? 2 * kTile + 128 : 0;  // bytes one TMA stage receives
+  // bytes one TMA stage receives
+  static constexpr int kTxBytes = kTma ? 2 * kTile + (KvTraits<KV>::kQuant ? 128 : 0) : 0;
   // chunk c of row r sits at chunk c ^ swz_bits(r): the 128-byte pattern
   // (r mod 8) for 128- and 256-byte rows, the 64-byte pattern ((r / 2) mod 4)
   // for 64-byte rows
@@ -237,14 +241,16 @@ __device__ __forceinline__ void issue_block(uint32_t wr, int st, const Args& a,
   if constexpr (S::kTma) {
     if (lane == 0) {
       const uint32_t bar = wr + S::kBarOff + 8 * st;
-      const uint32_t sz = wr + S::kSzOff + 128 * st;
-      const int64_t szi = (phys * a.kv_heads + h) * kBlock;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // after the reads of the last use
       mbar_arm(bar, S::kTxBytes);
       tma_tile_4d(kdst, &a.k_map, 0, h, 0, static_cast<int>(phys), bar);
       tma_tile_4d(vdst, &a.v_map, 0, h, 0, static_cast<int>(phys), bar);
-      bulk_copy(sz, a.k_sz + szi, 64, bar);
-      bulk_copy(sz + 64, a.v_sz + szi, 64, bar);
+      if constexpr (KvTraits<KV>::kQuant) {
+        const uint32_t sz = wr + S::kSzOff + 128 * st;
+        const int64_t szi = (phys * a.kv_heads + h) * kBlock;
+        bulk_copy(sz, a.k_sz + szi, 64, bar);
+        bulk_copy(sz + 64, a.v_sz + szi, 64, bar);
+      }
     }
   } else {
     const int64_t base = (phys * kBlock * a.kv_heads + h) * S::kRow;
@@ -284,7 +290,7 @@ __device__ __forceinline__ void read_frag(Frag<KV>& f, uint32_t wr, int st,
       f.v[r][0] = lds128(vt + lm.vr[r][0]);
       f.v[r][1] = lds128(vt + lm.vr[r][1]);
     }
-  } else if constexpr (KV == kI8) {
+  } else if constexpr (KV == kI8 || KV == kF8) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       f.k[0][i] = lds128(kt + lm.kr[0][i]);
@@ -320,6 +326,13 @@ __device__ __forceinline__ void k_operand(const Frag<KV>& f, int kk, uint32_t (&
     a[2] = w4(f.k[0][kk >> 1], (2 * kk + 1) & 3);
     a[1] = w4(f.k[1][kk >> 1], (2 * kk) & 3);
     a[3] = w4(f.k[1][kk >> 1], (2 * kk + 1) & 3);
+  } else if constexpr (KV == kF8) {  // fp16 whatever Q's type (q_to_f16)
+    const uint32_t w0 = w4(f.k[0][kk >> 2], kk & 3);
+    const uint32_t w1 = w4(f.k[1][kk >> 2], kk & 3);
+    a[0] = e4m3_lo_to_f16(w0);
+    a[2] = e4m3_hi_to_f16(w0);
+    a[1] = e4m3_lo_to_f16(w1);
+    a[3] = e4m3_hi_to_f16(w1);
   } else if constexpr (KV == kI8) {
     const uint32_t w0 = w4(f.k[0][kk >> 2], kk & 3);
     const uint32_t w1 = w4(f.k[1][kk >> 2], kk & 3);
@@ -357,6 +370,14 @@ __device__ __forceinline__ void v_operand(const Frag<KV>& f, int i, uint32_t (&a
     a[1] = prmt(r0, r1, 0x7632u);
     a[2] = prmt(r2, r3, 0x5410u);
     a[3] = prmt(r2, r3, 0x7632u);
+  } else if constexpr (KV == kF8) {
+    const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;  // bytes k, k+1 of two rows, k = 2(i%2)
+    const uint32_t x01 = prmt(w4(f.v[0], i >> 1), w4(f.v[1], i >> 1), sel);
+    const uint32_t x23 = prmt(w4(f.v[2], i >> 1), w4(f.v[3], i >> 1), sel);
+    a[0] = e4m3_lo_to_f16(x01);
+    a[1] = e4m3_hi_to_f16(x01);
+    a[2] = e4m3_lo_to_f16(x23);
+    a[3] = e4m3_hi_to_f16(x23);
   } else if constexpr (KV == kI8) {
     const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;  // bytes k, k+1 of two rows, k = 2(i%2)
     const uint32_t x01 = prmt(w4(f.v[0], i >> 1), w4(f.v[1], i >> 1), sel);
@@ -394,6 +415,59 @@ __device__ __forceinline__ void store_out(void* out, int64_t idx, float v) {
   } else {
     static_cast<__half*>(out)[idx] = __float2half_rn(v);
   }
+}
+
+// Clears the V rows of a fragment that lie outside tokens [lo, hi) of the
+// block: their weight is zero, but an infinity or a NaN there would still
+// reach the sum.
+template <int KV>
+__device__ __forceinline__ void clear_v_rows(Frag<KV>& f, int t, int lo, int hi) {
+  const int rows[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (rows[r] >= lo && rows[r] < hi) continue;
+    if constexpr (KV == kF16 || KV == kBF16) {
+      f.v[r][0] = f.v[r][1] = make_uint4(0u, 0u, 0u, 0u);
+    } else if constexpr (KV == kI8 || KV == kF8) {
+      f.v[r] = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      f.v[r] = make_uint2(0u, 0u);
+    }
+  }
+}
+
+// This lane's 32 dims of a bf16 query row (the four lanes of a quad hold the
+// row) as fp16, times a power of two that takes the row's largest element to
+// [2^14, 2^15): exact but for elements 2^28 times smaller than it. Returns the
+// inverse factor. For kernels that feed fp16 operands whatever Q's type.
+__device__ __forceinline__ float q_to_f16(uint32_t (&qw)[16]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = __vmaxu2(m, qw[i] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+  m = max(m, __shfl_xor_sync(kFull, m, 1));
+  m = max(m, __shfl_xor_sync(kFull, m, 2));
+  // factors 2^(14 - q) of the row's exponent q, kept to normal numbers
+  const int e = min(max(static_cast<int>(m >> 7), 16), 254);
+  const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+  const float down = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    qw[i] = pack2<false>(lo_to_float<true>(qw[i]) * up, hi_to_float<true>(qw[i]) * up);
+  return down;
+}
+
+// A score s (exp2 domain) capped: cap tanh(s / cap). Near zero by the series
+// of tanh (its next term is below 2^-24 of the sum there), else by
+// 1 - 2 / (1 + e^2x), whose error is about 2^-23 of the cap.
+__device__ __forceinline__ float softcap(const ScoreArgs& a, float s) {
+  const float x = s * a.cap_in, y = x * x;
+  const float u = ex2(x * 2.8853900817779268f);
+  const float far = 1.f - __fdividef(2.f, 1.f + u);
+  const float near =
+      x * fmaf(y, fmaf(y, fmaf(y, fmaf(y, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f),
+               1.f);
+  return a.cap * (y < 0.0625f ? near : far);
 }
 
 __host__ __device__ constexpr size_t align128(size_t x) { return (x + 127) / 128 * 128; }
