@@ -13,7 +13,7 @@
 //        block's first row (it starts the block anew),
 //   code = rne_e4m3(x 2^-(e' - 127)),
 //   and, where e' > e, every row that the run does not write:
-//   code' = rne_e4m3(code 2^(e - e')).
+//   code' = rne_e4m3(code 2^(e - e')), and 0 where e is 0.
 //
 // Work decomposition: a CTA takes the runs that begin in 16 consecutive
 // tokens, for one kv head of K or of V; a half-warp has one of the 32 rows
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kStoreThreads) store_fp8_kernel(const StoreArg
     // the block's other rows move to the new scale, shared out over the run's
     // half-warps; all loads before the first store
     const uint32_t by = now - old;
-    const float ratio = old == 0u || by > 30u ? 0.f : __uint_as_float((127u - by) << 23);
+    const float ratio = by > 30u ? 0.f : __uint_as_float((127u - by) << 23);
     const uint32_t keep = ~written & 0xFFFFu;
     const int n = end - lead;
     uint2 v[kBlock];
@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kStoreThreads) store_fp8_kernel(const StoreArg
     for (int o = 0; o < kBlock; ++o)
       if ((mine >> o) & 1u)
         *reinterpret_cast<uint2*>(tile + o * stride) =
-            make_uint2(rescale4(v[o].x, ratio), rescale4(v[o].y, ratio));
+            old == 0u ? make_uint2(0u, 0u)
+                      : make_uint2(rescale4(v[o].x, ratio), rescale4(v[o].y, ratio));
   }
 }
 
