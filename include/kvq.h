@@ -373,7 +373,7 @@ kvq_status paged_decode_attn_noalloc(const kvq_pool* pool, const void* q, int32_
  *                KVQ_EXTEND_MMA_SYNC (tiles of 16 rows on mma.sync; every pool
  *                kind; cuts long contexts into parts when the batch has few
  *                query tiles) or KVQ_EXTEND_TCGEN05 (units of 256 rows on
- *                tcgen05 with tensor-memory accumulators; INT8, INT4 and
+ *                tcgen05 with tensor-memory accumulators; FP8, INT8, INT4 and
  *                fp16 pools of at least one block, at most 4096 requests;
  *                KVQ_ERR_UNSUPPORTED otherwise). AUTO takes the tcgen05 kernel when it accepts
  *                the call and the batch has at least as many 256-row units

@@ -624,7 +624,7 @@ static kvq_status extend_impl(const kvq_pool* pool, const kvq_score* score, cons
   const bool scored = score != nullptr &&
                       (score->softcap > 0.f || score->window > 0 ||
                        score->alibi_slopes != nullptr || score->prefix_lens != nullptr);
-  const bool tc_ok = !scored && kvq::extend_tc_supported(pool->kv_dtype, q_dtype) &&
+  const bool tc_ok = kvq::extend_tc_supported(pool->kv_dtype, q_dtype) &&
                      batch <= kvq::extend_tc_max_batch() && pool->num_blocks > 0;
   if (variant == KVQ_EXTEND_TCGEN05 && !tc_ok) return KVQ_ERR_UNSUPPORTED;
   if (batch > kvq::kMaxBatch) return KVQ_ERR_UNSUPPORTED;
@@ -683,6 +683,14 @@ static kvq_status extend_impl(const kvq_pool* pool, const kvq_score* score, cons
                       (variant == KVQ_EXTEND_AUTO && tc_ok && tc_units >= sms);
   if (use_tc) {
     // persistent CTAs, one per SM (each holds all 512 TMEM columns)
+    if (fp8 || scored) {
+      if (kvq::extend_tc_scored_ctas_per_sm(pool->kv_dtype, q_dtype, scored, batch) <= 0)
+        return KVQ_ERR_CUDA;
+      return kvq::launch_extend_tc_scored(a, pool->kv_dtype, q_dtype, scored, sms, s) ==
+                     cudaSuccess
+                 ? KVQ_OK
+                 : KVQ_ERR_CUDA;
+    }
     if (kvq::extend_tc_ctas_per_sm(pool->kv_dtype, q_dtype, batch) <= 0) return KVQ_ERR_CUDA;
     return kvq::launch_extend_tc(a, pool->kv_dtype, q_dtype, sms, s) == cudaSuccess
                ? KVQ_OK

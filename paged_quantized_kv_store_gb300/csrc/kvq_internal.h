@@ -190,11 +190,15 @@ int extend_ctas_per_sm(int kv_dtype, int q_dtype, int batch);
 cudaError_t launch_extend_scored(const ExtendArgs& a, int kv_dtype, int q_dtype, bool scored,
                                  int grid_ctas, cudaStream_t s);
 int extend_scored_ctas_per_sm(int kv_dtype, int q_dtype, bool scored, int batch);
-// the tcgen05 version (256-row units; INT8, INT4 and fp16 pools)
+// the tcgen05 version (256-row units; FP8, INT8, INT4 and fp16 pools); the FP8
+// and scored kernels are launched apart (kvq_extend_tc_scored.cu)
 bool extend_tc_supported(int kv_dtype, int q_dtype);
 cudaError_t launch_extend_tc(const ExtendArgs& a, int kv_dtype, int q_dtype, int grid_ctas,
                              cudaStream_t s);
 int extend_tc_ctas_per_sm(int kv_dtype, int q_dtype, int batch);
+cudaError_t launch_extend_tc_scored(const ExtendArgs& a, int kv_dtype, int q_dtype, bool scored,
+                                    int grid_ctas, cudaStream_t s);
+int extend_tc_scored_ctas_per_sm(int kv_dtype, int q_dtype, bool scored, int batch);
 int extend_tc_max_batch();                // most requests the tcgen05 kernel takes
 cudaError_t launch_copy(const CopyArgs& a, int64_t n, cudaStream_t s);
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t s);

@@ -230,7 +230,7 @@ def test_fp8_v_scales_far_apart(gpu, form, hkv):
     else:
         indptr = [0, 300, 390, 391]
         q = randn(9, 391, 4 * hkv, 128, dtype="bf16")
-        for variant in ("mma_sync", "auto"):
+        for variant in ("mma_sync", "tcgen05"):
             compare(pool, run_extend(pool, q, bt, lens, indptr, variant=variant), q, bt, lens, indptr)
 
 
@@ -247,7 +247,7 @@ def test_fp8_blocks_of_zeros(gpu):
     compare(pool, run_decode(pool, q, bt, lens), q, bt, lens)
     indptr = [0, 90, 130]
     q = randn(10, 130, 8, 128)
-    for variant in ("mma_sync", "auto"):
+    for variant in ("mma_sync", "tcgen05"):
         compare(pool, run_extend(pool, q, bt, lens, indptr, variant=variant), q, bt, lens, indptr)
 
 
@@ -302,7 +302,7 @@ CTX = [[777], [40, 50, 1, 400, 18, 300], [600, 900]]
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("variant", ["mma_sync", "auto"])
+@pytest.mark.parametrize("variant", ["mma_sync", "tcgen05"])
 @pytest.mark.parametrize("hq,hkv", [(8, 8), (32, 8), (15, 5), (16, 1)])
 def test_extend_fp8(gpu, dtype, variant, hq, hkv):
     for c, lens in zip(CHUNKS, CTX):
@@ -325,7 +325,44 @@ def test_extend_scored(gpu, kind, dtype, combo):
         indptr = np.concatenate([[0], np.cumsum(c)])
         q = randn(28, int(indptr[-1]), 12, 128, dtype=dtype, scale=2.0)
         s, kw = score_of(combo, 12, len(lens), lens)
-        compare(pool, run_extend(pool, q, bt, lens, indptr, s), q, bt, lens, indptr, **kw)
+        for variant in ("mma_sync",) if kind == "bf16" else ("mma_sync", "tcgen05"):
+            out = run_extend(pool, q, bt, lens, indptr, s, variant)
+            compare(pool, out, q, bt, lens, indptr, **kw)
+
+
+@pytest.mark.parametrize("variant", ["mma_sync", "tcgen05"])
+@pytest.mark.parametrize("cap", [1e-6, 0.5, 8.0, 50.0, 1e6])
+def test_extend_caps(gpu, variant, cap):
+    """Scores far below the cap, near it and beyond it in one tile."""
+    lens, indptr = [150, 70], [0, 140, 200]
+    pool, bt = make_pool("fp8", lens, 2, 41)
+    q = randn(29, 200, 8, 128, scale=8.0)
+    q[::3] *= 0.05
+    out = run_extend(pool, q, bt, lens, indptr, kvq.Score(cap), variant)
+    compare(pool, out, q, bt, lens, indptr, cap=cap)
+
+
+@pytest.mark.parametrize("variant", ["mma_sync", "tcgen05"])
+@pytest.mark.parametrize("window", [1, 16, 63, 64, 65, 300, 5000])
+def test_extend_windows(gpu, variant, window):
+    """Windows shorter than a tile, at its size and longer than the context."""
+    lens, indptr = [900, 70], [0, 700, 770]
+    pool, bt = make_pool("fp8", lens, 2, 42, "bf16")
+    q = randn(30, 770, 4, 128, dtype="bf16")
+    out = run_extend(pool, q, bt, lens, indptr, kvq.Score(window=window), variant)
+    compare(pool, out, q, bt, lens, indptr, window=window)
+
+
+@pytest.mark.parametrize("variant", ["mma_sync", "tcgen05"])
+@pytest.mark.parametrize("scale", [0.0, -0.09])
+def test_extend_other_softmax_scales(gpu, monkeypatch, variant, scale):
+    monkeypatch.setitem(globals(), "SM", scale)
+    lens, indptr = [200, 70], [0, 140, 200]
+    pool, bt = make_pool("fp8", lens, 2, 43)
+    q = randn(31, 200, 8, 128)
+    for s, kw in ((None, {}), score_of("cwap", 8, 2, lens)):
+        out = run_extend(pool, q, bt, lens, indptr, s, variant)
+        compare(pool, out, q, bt, lens, indptr, **kw)
 
 
 # ---- together, and as programs call them ---------------------------------------------
@@ -438,7 +475,7 @@ def test_offsets_past_32_bits(gpu):
     a, b = run_decode(pool, q, bt, [n]), run_decode(small, q, ids, [n])
     assert torch.equal(a, b)
     q = randn(83, n, 32, 128)
-    for variant in ("mma_sync", "auto"):
+    for variant in ("mma_sync", "tcgen05"):
         a = run_extend(pool, q, bt, [n], [0, n], variant=variant)
         assert torch.equal(a, run_extend(small, q, ids, [n], [0, n], variant=variant))
     compare(small, a, q, ids, [n], [0, n])
