@@ -420,6 +420,35 @@ ExtendPlan extend_plan(int batch, int total_q, int q_heads, int kv_heads, int ma
   return p;
 }
 
+// The same for the tcgen05 kernels that can cut the context (FP8 pools, and
+// scores): parts of whole 64-token tiles, at least 4 of them, so that about two
+// units for each SM are at hand; at most 16 parts (the combine takes 32).
+// Measured for 7 ragged chunks over 700 to 4000 tokens (about 150 units):
+// 376 us on mma.sync, and on tcgen05 PLACEHOLDER whole and cut.
+ExtendPlan extend_tc_plan(int total_q, int q_heads, int kv_heads, int max_kv_len, int num_sms) {
+  ExtendPlan p;
+  const int group = q_heads / kv_heads;
+  const int64_t units = static_cast<int64_t>(kv_heads) *
+                        ((static_cast<int64_t>(total_q) * group + 255) / 256);
+  const int nblk = std::max(1, (max_kv_len + kBlock - 1) / kBlock);
+  p.pchunk = 0;
+  p.max_splits = 1;
+  if (units > 0 && units < 2 * num_sms) {
+    const int want = static_cast<int>(std::min<int64_t>(16, (2 * num_sms + units - 1) / units));
+    const int chunk = std::max(16, ((nblk + want - 1) / want + 3) / 4 * 4);
+    const int splits = (nblk + chunk - 1) / chunk;
+    if (splits > 1) {
+      p.pchunk = chunk;
+      p.max_splits = splits;
+    }
+  }
+  p.part_off = 256;
+  p.total = p.part_off + (p.pchunk > 0 ? static_cast<size_t>(total_q) * q_heads * p.max_splits *
+                                             kvq::kPartStride * sizeof(float)
+                                       : 0);
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -598,7 +627,8 @@ kvq_status paged_extend_attn_workspace_size(int32_t batch, int32_t total_q, int3
   if (head_dim != kHeadDim) return KVQ_ERR_UNSUPPORTED;
   const int sms = current_sm_count();
   if (sms <= 0) return KVQ_ERR_CUDA;
-  *bytes = extend_plan(batch, total_q, q_heads, kv_heads, max_kv_len, sms).total;
+  *bytes = std::max(extend_plan(batch, total_q, q_heads, kv_heads, max_kv_len, sms).total,
+                    extend_tc_plan(total_q, q_heads, kv_heads, max_kv_len, sms).total);
   return KVQ_OK;
 }
 
@@ -635,8 +665,23 @@ static kvq_status extend_impl(const kvq_pool* pool, const kvq_score* score, cons
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return KVQ_ERR_INVALID_ARG;
   const int sms = current_sm_count();
   if (sms <= 0) return KVQ_ERR_CUDA;
+  // tcgen05 (256-row units) when the pool kind allows it and the batch has at
+  // least one unit per SM; else 16-row tiles on mma.sync (which can also cut
+  // the context of a short chunk into parts). The FP8 and scored tcgen05
+  // kernels can cut it too, so there the rows of a request count: a 256-row
+  // unit with fewer than about 96 rows in use costs more than 16-row tiles.
+  const int group = q_heads / pool->kv_heads;
+  const int64_t tc_units = static_cast<int64_t>(pool->kv_heads) *
+                           ((static_cast<int64_t>(total_q) * group + 255) / 256);
+  const bool tc_pays = fp8 || scored
+                           ? static_cast<int64_t>(total_q) * group >= int64_t{96} * batch
+                           : tc_units >= sms;
+  const bool use_tc = variant == KVQ_EXTEND_TCGEN05 ||
+                      (variant == KVQ_EXTEND_AUTO && tc_ok && tc_pays);
   const ExtendPlan plan =
-      extend_plan(batch, total_q, q_heads, pool->kv_heads, max_kv_len, sms);
+      use_tc && (fp8 || scored)
+          ? extend_tc_plan(total_q, q_heads, pool->kv_heads, max_kv_len, sms)
+          : extend_plan(batch, total_q, q_heads, pool->kv_heads, max_kv_len, sms);
   if (workspace == nullptr || workspace_bytes < plan.total) return KVQ_ERR_WORKSPACE;
   kvq::ExtendArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -674,13 +719,6 @@ static kvq_status extend_impl(const kvq_pool* pool, const kvq_score* score, cons
   a.dev_err = dev_err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(a.counter, 0, sizeof(int32_t), s) != cudaSuccess) return KVQ_ERR_CUDA;
-  // tcgen05 (256-row units) when the pool kind allows it and the batch has at
-  // least one unit per SM; else 16-row tiles on mma.sync (which can also cut
-  // the context of a short chunk into parts)
-  const int64_t tc_units = static_cast<int64_t>(pool->kv_heads) *
-                           ((static_cast<int64_t>(total_q) * a.group + 255) / 256);
-  const bool use_tc = variant == KVQ_EXTEND_TCGEN05 ||
-                      (variant == KVQ_EXTEND_AUTO && tc_ok && tc_units >= sms);
   if (use_tc) {
     // persistent CTAs, one per SM (each holds all 512 TMEM columns)
     if (fp8 || scored) {

@@ -594,6 +594,14 @@ __global__ void __launch_bounds__(128) extend_combine_kernel(const __grid_consta
   reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + rh * kHeadDim)[lane] = w;
 }
 
+template <bool QBF>
+cudaError_t launch_combine_t(const ExtendArgs& a, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(a.total_q) * a.q_heads;
+  if (rows == 0) return cudaSuccess;
+  extend_combine_kernel<QBF><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <int KV, bool QBF, bool SC = false>
 cudaError_t launch_t(const ExtendArgs& a, int grid, cudaStream_t s) {
   thread_local int opted_in_device = -1;  // per host thread: no shared state
@@ -609,10 +617,7 @@ cudaError_t launch_t(const ExtendArgs& a, int grid, cudaStream_t s) {
   extend_kernel<KV, QBF, SC><<<grid, kDecodeThreads, extend_smem_bytes<KV>(a.batch), s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.pchunk == 0) return e;
-  const int64_t rows = static_cast<int64_t>(a.total_q) * a.q_heads;
-  if (rows == 0) return cudaSuccess;
-  extend_combine_kernel<QBF><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_combine_t<QBF>(a, s);
 }
 
 template <int KV, bool QBF, bool SC = false>

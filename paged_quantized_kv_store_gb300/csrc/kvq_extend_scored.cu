@@ -54,6 +54,10 @@ cudaError_t launch_extend_scored(const ExtendArgs& a, int kv_dtype, int q_dtype,
   return with_kinds(kv_dtype, q_dtype, scored, Launch{a, grid, s});
 }
 
+cudaError_t launch_extend_combine(const ExtendArgs& a, bool out_bf16, cudaStream_t s) {
+  return out_bf16 ? launch_combine_t<true>(a, s) : launch_combine_t<false>(a, s);
+}
+
 int extend_scored_ctas_per_sm(int kv_dtype, int q_dtype, bool scored, int batch) {
   return with_kinds(kv_dtype, q_dtype, scored, Occupancy{batch});
 }

@@ -69,6 +69,8 @@ constexpr uint32_t raw_tx() {  // bytes the copies of a stage bring
 }
 constexpr uint32_t kRawBytes = (kRawValidOff + 16 + 1023) / 1024 * 1024;
 constexpr uint32_t kRawOff = (kInfoOff + kStages * 16 + 1023) / 1024 * 1024;
+template <int KV, bool SC>
+constexpr bool can_split() { return KV == kF8 || SC; }
 template <int KV>
 constexpr bool raw_ring() { return KV == kI8 || KV == kF8; }
 // FP8 pools: a raw stage's words at kRawValidOff are the valid bits, then the
@@ -110,9 +112,14 @@ static_assert(tc_smem_bytes(kTcMaxBatch) + 1024 <= 232448, "shared memory over t
 
 struct TcReq {
   int q0, C, L, tiles;
+  int splits;  // parts that the context is cut into (1 where it is not)
   bool ok;
 };
 
+// SPLIT: the kernels that can cut a request's context into parts of a.pchunk
+// blocks (a whole number of tiles), each a work unit of its own with a record
+// that extend_combine_kernel merges. One part otherwise.
+template <bool SPLIT>
 __device__ __forceinline__ TcReq tc_req(const ExtendArgs& a, int b) {
   TcReq s;
   s.q0 = a.qo_indptr[b];
@@ -122,6 +129,10 @@ __device__ __forceinline__ TcReq tc_req(const ExtendArgs& a, int b) {
   s.ok = s.q0 >= 0 && s.C >= 0 && q1 <= a.total_q && s.L >= s.C && s.L <= a.len_cap;
   if (!s.ok) s.C = s.L = 0;
   s.tiles = (s.C * a.group + kUnitRows - 1) / kUnitRows;
+  s.splits = 1;
+  if constexpr (SPLIT) {
+    if (a.pchunk > 0) s.splits = max(((s.L + kBlock - 1) / kBlock + a.pchunk - 1) / a.pchunk, 1);
+  }
   return s;
 }
 
@@ -644,16 +655,23 @@ __device__ __forceinline__ uint32_t ex2_h2(uint32_t h) {
   return r;
 }
 
-// tanh(x) / x by its series in y = x^2 up to x^16 (|x| < 0.6: the next term is
-// below 2^-23 of the sum).
+// tanh(x) / x as a polynomial in y = x^2, |x| <= 1.25: the Chebyshev
+// interpolant of degree 7 over [0, 1.5625] (tanh's poles at +-i pi / 2 lie at
+// y = -2.47, so its coefficients fall by a factor of 8 each); relative error
+// below 2.3e-7 in fp32.
 __device__ __forceinline__ float2 tanh_over_x(float2 y) {
-  constexpr float k[8] = {-1.f / 3.f, 2.f / 15.f, -17.f / 315.f, 62.f / 2835.f,
-                          -1382.f / 155925.f, 21844.f / 6081075.f, -929569.f / 638512875.f,
-                          6404582.f / 10854718875.f};
+  constexpr float k[8] = {0.99999994f,   -0.33332729f,  0.13324812f,    -0.05350182f,
+                          0.020577831f,  -0.0068152983f, 0.0015969310f, -0.00018419606f};
   float2 p = make_float2(k[7], k[7]);
 #pragma unroll
   for (int i = 6; i >= 0; --i) p = __ffma2_rn(p, y, make_float2(k[i], k[i]));
-  return __ffma2_rn(p, y, make_float2(1.f, 1.f));
+  return p;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // One fp32 column of this thread's TMEM lane.
@@ -683,7 +701,7 @@ __device__ __forceinline__ void score_tile(const ScoreArgs& a, float slope, int 
     float mx = 0.f;
 #pragma unroll
     for (int t = 0; t < kTcTok; t += 2) mx = max3(mx, fabsf(x[t]), fabsf(x[t + 1]));
-    if (__all_sync(kFull, mx * a.cap_in < 0.6f)) {
+    if (__all_sync(kFull, mx * a.cap_in < 1.25f)) {
       const float2 in2 = make_float2(a.cap_in, a.cap_in);
 #pragma unroll
       for (int t = 0; t < kTcTok; t += 2) {
@@ -696,7 +714,7 @@ __device__ __forceinline__ void score_tile(const ScoreArgs& a, float slope, int 
       const float in = a.cap_in * 2.8853900817779268f;
 #pragma unroll
       for (int t = 0; t < kTcTok; ++t)
-        x[t] = fmaf(-2.f * a.cap, __frcp_rn(1.f + ex2(x[t] * in)), a.cap);
+        x[t] = fmaf(-2.f * a.cap, rcp(1.f + ex2(x[t] * in)), a.cap);
     }
   }
   if (slope != 0.f) {
@@ -817,7 +835,8 @@ __device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f) {
 
 struct TcUnit {
   int b, h, qt, ntiles;
-  int j0;    // first context tile (0 without a window)
+  int c;     // part of the context
+  int j0;    // first context tile (0 without a window, in the first part)
   int plen;  // tokens that every row sees (0 without a prefix)
   TcReq s;
 };
@@ -825,8 +844,9 @@ struct TcUnit {
 // Unit u: request b (by the prefix sums of units per request), kv head h and
 // 256-row tile qt (longest first), with the 64-token context tiles its rows
 // attend: those up to its last query's position, or (SC) up to the prefix's
-// end and from the window of its first query on.
-template <bool SC>
+// end and from the window of its first query on; of these, its part's (none,
+// possibly).
+template <bool SC, bool SPLIT>
 __device__ __forceinline__ TcUnit tc_unit(const ExtendArgs& a, const int32_t* ucum, int u) {
   int lo = 0, hi = a.batch - 1;
   while (lo < hi) {
@@ -835,8 +855,13 @@ __device__ __forceinline__ TcUnit tc_unit(const ExtendArgs& a, const int32_t* uc
   }
   TcUnit w;
   w.b = lo;
-  w.s = tc_req(a, lo);
-  const int r = u - ucum[lo];
+  w.s = tc_req<SPLIT>(a, lo);
+  int r = u - ucum[lo];
+  w.c = 0;
+  if constexpr (SPLIT) {
+    w.c = r % w.s.splits;
+    r /= w.s.splits;
+  }
   w.h = r % a.kv_heads;
   w.qt = w.s.tiles - 1 - r / a.kv_heads;
   const int i_max = min(w.s.C - 1, (w.qt * kUnitRows + kUnitRows - 1) / a.group);
@@ -850,7 +875,15 @@ __device__ __forceinline__ TcUnit tc_unit(const ExtendArgs& a, const int32_t* uc
     if (a.score.window > 0)
       w.j0 = max(w.s.L - w.s.C + (w.qt * kUnitRows) / a.group - a.score.window + 1, 0) / kTcTok;
   }
-  w.ntiles = (n_tok + kTcTok - 1) / kTcTok - w.j0;
+  int j1 = (n_tok + kTcTok - 1) / kTcTok;
+  if constexpr (SPLIT) {
+    if (w.s.splits > 1) {
+      const int per = a.pchunk * kBlock / kTcTok;
+      w.j0 = max(w.j0, w.c * per);
+      j1 = min(j1, (w.c + 1) * per);
+    }
+  }
+  w.ntiles = max(j1 - w.j0, 0);
   return w;
 }
 
@@ -906,7 +939,7 @@ __device__ __forceinline__ void staging_role(const ExtendArgs& a, const TcShared
     __syncwarp();
     if (lane == 0) mbar_arrive_one(c.bar(kBarUnitEmpty + slot));
     if (u >= c.total) return;
-    const TcUnit w = tc_unit<SC>(a, c.ucum, u);
+    const TcUnit w = tc_unit<SC, can_split<KV, SC>()>(a, c.ucum, u);
     const int n = w.ntiles, L = w.s.L, tokb = w.j0 * kTcTok;
     uint32_t vref = 0u;  // FP8 pools: the unit's reference scale
     // registers -> the next K/V stage
@@ -979,7 +1012,7 @@ __device__ __forceinline__ void producer_role(const ExtendArgs& a, const TcShare
     __syncwarp();
     if (lane == 0) mbar_arrive_one(c.bar(kBarUnitEmpty + slot));
     if (u >= c.total) break;
-    const TcUnit w = tc_unit<SC>(a, c.ucum, u);
+    const TcUnit w = tc_unit<SC, can_split<KV, SC>()>(a, c.ucum, u);
     const int32_t* bt = a.block_tables + static_cast<int64_t>(w.b) * a.max_blocks;
     const int tokb = w.j0 * kTcTok;
     int4 blk = tile_blocks(bt, tokb, a.max_blocks);
@@ -1068,7 +1101,7 @@ __device__ __forceinline__ bool elect_one() {
 // elected lane issues each product and commit. The two warpgroups' products
 // need no order between them; a K/V stage is released when both MMA warps
 // have committed its products (the empty barrier takes two arrivals).
-template <bool QBF, bool EX, bool SC>
+template <bool QBF, bool EX, bool SC, bool SPLIT>
 __device__ __forceinline__ void mma_role(const ExtendArgs& a, const TcShared& c, int g,
                                          int lane) {
   constexpr uint32_t idesc_s = umma_idesc_f16(QBF, kWgRows, kTcTok);
@@ -1114,8 +1147,9 @@ __device__ __forceinline__ void mma_role(const ExtendArgs& a, const TcShared& c,
     __syncwarp();
     if (lane == 0) mbar_arrive_one(c.bar(kBarUnitEmpty + slot));
     if (u >= c.total) return;
-    const int n = tc_unit<SC>(a, c.ucum, u).ntiles;
+    const int n = tc_unit<SC, SPLIT>(a, c.ucum, u).ntiles;
     if (!wait(c.bar(kBarQFull + g), k & 1u)) return;
+    if (SPLIT && n == 0) continue;
     if (!wait(c.bar(kBarKvFull + tc % kStages), (tc / kStages) & 1u)) return;
     issue_s(tc % kStages);
     for (int j = 0; j < n; ++j, ++tc) {
@@ -1158,7 +1192,7 @@ __device__ __forceinline__ void softmax_role(const ExtendArgs& a, const TcShared
     __syncwarp();
     if (lane == 0) mbar_arrive_one(c.bar(kBarUnitEmpty + slot));
     if (u >= c.total) return;
-    const TcUnit w = tc_unit<SC>(a, c.ucum, u);
+    const TcUnit w = tc_unit<SC, can_split<KV, SC>()>(a, c.ucum, u);
     const int row = w.qt * kUnitRows + g * kWgRows + i;
     const int qi = row / a.group;
     const int hq = w.h * a.group + row % a.group;
@@ -1398,9 +1432,34 @@ __device__ __forceinline__ void softmax_role(const ExtendArgs& a, const TcShared
       mbar_arrive_one(c.bar(kBarPFull + g));
     }
     // output row: (O + z) / l (every lane takes part in the TMEM reads)
-    if (!wait(c.bar(kBarODone + g), (tc - 1u) & 1u)) return;
+    if (w.ntiles > 0 && !wait(c.bar(kBarODone + g), (tc - 1u) & 1u)) return;
     tc_fence_after();
-    {
+    if (can_split<KV, SC>() && w.s.splits > 1) {  // the part's record: O, maximum, sum
+      float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+      const float z = (z2[0].x + z2[0].y) + (z2[1].x + z2[1].y);
+      float* rec = a.part + (((static_cast<int64_t>(w.s.q0) + qi) * a.q_heads + hq) * a.max_splits +
+                             w.c) * kPartStride;
+      if (w.ntiles > 0) {
+        if constexpr (kVDeq) l = tmem_ld1(o_addr + kHeadDim);
+#pragma unroll 1
+        for (int cc = 0; cc < 4; ++cc) {
+          float v[32];
+          tmem_ld32(o_addr + 32 * cc, v);
+          if (valid) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              reinterpret_cast<float4*>(rec + 32 * cc)[q] =
+                  make_float4((v[4 * q] + z) * unit, (v[4 * q + 1] + z) * unit,
+                              (v[4 * q + 2] + z) * unit, (v[4 * q + 3] + z) * unit);
+          }
+        }
+      } else if (valid) {
+#pragma unroll 1
+        for (int q = 0; q < kHeadDim / 4; ++q)
+          reinterpret_cast<float4*>(rec)[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if (valid) *reinterpret_cast<float2*>(rec + kHeadDim) = make_float2(m, l);
+    } else {
       float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
       const float z = (z2[0].x + z2[0].y) + (z2[1].x + z2[1].y);
       if constexpr (kVDeq) l = tmem_ld1(o_addr + kHeadDim);  // the row-sum column
@@ -1430,6 +1489,7 @@ __device__ __forceinline__ void softmax_role(const ExtendArgs& a, const TcShared
 
 template <int KV, bool QBF, bool OBF = QBF, bool SC = false, bool EX = QBF>
 __global__ void __launch_bounds__(kTcThreads, 1) extend_tc_kernel(const __grid_constant__ ExtendArgs a) {
+  constexpr bool kSplit = can_split<KV, SC>();
   extern __shared__ __align__(1024) unsigned char dsmem[];
   __shared__ int32_t warp_sum[kTcThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1444,8 +1504,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) extend_tc_kernel(const __grid_c
     const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
     int sum = 0;
     for (int b = b0; b < b1; ++b) {
-      const TcReq s = tc_req(a, b);
-      sum += a.kv_heads * s.tiles;
+      const TcReq s = tc_req<kSplit>(a, b);
+      sum += a.kv_heads * s.tiles * s.splits;
       if (blockIdx.x == 0 && !s.ok) report(a.dev_err, KVQ_DEV_ERR_LENGTH);
     }
     int incl = sum;
@@ -1461,7 +1521,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) extend_tc_kernel(const __grid_c
     int run = basec + incl - sum;
     for (int b = b0; b < b1; ++b) {
       ucum[b] = run;
-      run += a.kv_heads * tc_req(a, b).tiles;
+      const TcReq s = tc_req<kSplit>(a, b);
+      run += a.kv_heads * s.tiles * s.splits;
     }
     if (tid == kTcThreads - 1) ucum[a.batch] = basec + incl;
   }
@@ -1509,7 +1570,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) extend_tc_kernel(const __grid_c
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
     if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-      mma_role<QBF, EX, SC>(a, c, warp - kMmaWarp, lane);
+      mma_role<QBF, EX, SC, kSplit>(a, c, warp - kMmaWarp, lane);
       // every product either MMA warp issued completes before the TMEM is freed
       __syncwarp();
       if (elect_one()) {
@@ -1548,7 +1609,9 @@ cudaError_t launch_tc_t(const ExtendArgs& a, int grid, cudaStream_t s) {
     opted_in_device = dev;
   }
   extend_tc_kernel<KV, QBF, OBF, SC, EX><<<grid, kTcThreads, tc_smem_bytes(a.batch), s>>>(a);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !can_split<KV, SC>() || a.pchunk == 0) return e;
+  return launch_extend_combine(a, OBF, s);
 }
 
 template <int KV, bool QBF, bool OBF = QBF, bool SC = false, bool EX = QBF>

@@ -190,6 +190,8 @@ int extend_ctas_per_sm(int kv_dtype, int q_dtype, int batch);
 cudaError_t launch_extend_scored(const ExtendArgs& a, int kv_dtype, int q_dtype, bool scored,
                                  int grid_ctas, cudaStream_t s);
 int extend_scored_ctas_per_sm(int kv_dtype, int q_dtype, bool scored, int batch);
+// merges the records of requests whose context was cut into a.pchunk blocks
+cudaError_t launch_extend_combine(const ExtendArgs& a, bool out_bf16, cudaStream_t s);
 // the tcgen05 version (256-row units; FP8, INT8, INT4 and fp16 pools); the FP8
 // and scored kernels are launched apart (kvq_extend_tc_scored.cu)
 bool extend_tc_supported(int kv_dtype, int q_dtype);
