@@ -149,10 +149,18 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = None  # the current stream's handle, without a Stream object around it
+
+
 def _stream(stream) -> Optional[int]:
+    global _raw_stream
     if stream is None:
-        import torch
-        stream = torch.cuda.current_stream()
+        if _raw_stream is None:
+            import torch
+            torch.cuda.init()
+            get, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+            _raw_stream = lambda: get(device())  # noqa: E731
+        return _raw_stream() or None
     h = getattr(stream, "cuda_stream", stream)
     return h or None
 

@@ -20,6 +20,11 @@ namespace {
 
 constexpr int kAutoMinBlocksPerWarp = 4;  // a warp's range is never shorter than this
 constexpr float kMinSoftcap = 1e-6f, kMaxSoftcap = 1e6f;
+#ifndef WHOLE
+#define WHOLE 256
+#endif
+constexpr int kWholeTokens = WHOLE;  // longest context a warp attends alone
+constexpr int kWideRows = 8;  // rows for each SM up to which a CTA merges each
 
 // Decode workspace: [256 bytes: the tail-chunk counter, the fused step's
 // barrier counter][header: 4 ints + batch + 1 prefix sums][partial records:
@@ -370,6 +375,14 @@ kvq_status decode_impl(const kvq_pool* pool, const void* q, int32_t q_dtype, voi
         kvq::decode_scored_ctas_per_sm(pool->kv_dtype, q_dtype, scored, batch),
         kvq::kMaxCtasPerSm);
     if (per_sm <= 0) return KVQ_ERR_CUDA;
+    // short contexts, few enough for a warp each: a request is not cut, and
+    // nothing is left to merge
+    const int seen = scored && score->window > 0 && score->window < max_seq_len - kBlock
+                         ? score->window + kBlock
+                         : max_seq_len;
+    a.whole = num_splits == 0 && seen <= kWholeTokens &&
+              static_cast<int64_t>(batch) * pool->kv_heads * plan.head_groups <=
+                  static_cast<int64_t>(plan.num_sms) * per_sm * (kvq::kDecodeThreads / 32);
     if (kvq::launch_decode_scored(a, pool->kv_dtype, q_dtype, scored, plan.num_sms * per_sm, s) !=
         cudaSuccess)
       return KVQ_ERR_CUDA;
@@ -381,6 +394,10 @@ kvq_status decode_impl(const kvq_pool* pool, const void* q, int32_t q_dtype, voi
         cudaSuccess)
       return KVQ_ERR_CUDA;
   }
+  if (a.whole) return KVQ_OK;
+  // few rows of many pieces: a CTA for each
+  if ((fp8 || scored) && static_cast<int64_t>(batch) * q_heads <= kWideRows * plan.num_sms)
+    return kvq::launch_combine_wide(a, q_dtype, s) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
   if (kvq::launch_combine(a, q_dtype, s) != cudaSuccess) return KVQ_ERR_CUDA;
   return KVQ_OK;
 }

@@ -82,10 +82,22 @@ __global__ void __launch_bounds__(kDecodeThreads, TAIL && KV != kI4 ? 3 : 1)
 // range), then its shared-prefix records, if any (a request made of shared
 // blocks only has nothing else). Log-sum-exp in the exp2 domain, 8 pieces
 // per round of loads.
-template <bool QBF>
+// The pieces a row has: records of ranges r_first .. r_first + nd - 1 of the
+// decode, then npc shared-prefix records; nd + npc = 0 for a row that needs no
+// merge.
+struct Pieces {
+  int64_t r_first, nd, seg_start;
+  int hh, npc;
+  RangeMap rm;
+};
+
+// W = 1: by one warp. W > 1: by the W warps of a CTA, each every W-th batch of
+// pieces, joined in shared memory (sh) at the end.
+template <bool QBF, int W = 1>
 __device__ __forceinline__ void merge_pieces(const DecodeArgs& a, int64_t bh, int hh, int lane,
                                              int64_t r_first, int64_t nd, int64_t seg_start,
-                                             const RangeMap& rm, int npc) {
+                                             const RangeMap& rm, int npc, int warp = 0,
+                                             float (*sh)[kPartStride] = nullptr) {
   auto rec_of = [&](int64_t i) -> const float* {
     if (i < nd) {
       const int slot = (i == 0 && seg_start != range_start(rm, r_first)) ? 1 : 0;
@@ -97,7 +109,7 @@ __device__ __forceinline__ void merge_pieces(const DecodeArgs& a, int64_t bh, in
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float lsum = 0.f, M = -INFINITY;
   constexpr int kBatch = 8;  // pieces whose loads are in flight together
-  for (int64_t base = 0; base < npieces; base += kBatch) {
+  for (int64_t base = kBatch * warp; base < npieces; base += W * kBatch) {
     // every lane reads each piece's maximum and sum (one address: broadcast)
     // and its own 4 columns, all loads of the batch issued before any use;
     // through L2, as other SMs wrote the records
@@ -133,6 +145,27 @@ __device__ __forceinline__ void merge_pieces(const DecodeArgs& a, int64_t bh, in
       acc.x += e * x[i].x; acc.y += e * x[i].y; acc.z += e * x[i].z; acc.w += e * x[i].w;
     }
   }
+  if constexpr (W > 1) {
+    reinterpret_cast<float4*>(sh[warp])[lane] = acc;
+    if (lane == 0) {
+      sh[warp][kHeadDim] = M;
+      sh[warp][kHeadDim + 1] = lsum;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < W; ++i) M = fmaxf(M, sh[i][kHeadDim]);
+    lsum = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float m = sh[i][kHeadDim], e = m == -INFINITY ? 0.f : exp2f(m - M);
+      const float4 x = reinterpret_cast<const float4*>(sh[i])[lane];
+      lsum += e * sh[i][kHeadDim + 1];
+      acc.x += e * x.x; acc.y += e * x.y; acc.z += e * x.z; acc.w += e * x.w;
+    }
+  }
   const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
   uint2 w;
   w.x = pack2<QBF>(acc.x * inv, acc.y * inv);
@@ -140,13 +173,15 @@ __device__ __forceinline__ void merge_pieces(const DecodeArgs& a, int64_t bh, in
   reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + bh * kHeadDim)[lane] = w;
 }
 
-template <bool QBF>
-__device__ __forceinline__ void combine_row(const DecodeArgs& a, int64_t bh, int lane) {
-  if (bh >= static_cast<int64_t>(a.batch) * a.q_heads) return;
+__device__ __forceinline__ Pieces pieces_of(const DecodeArgs& a, int64_t bh) {
+  Pieces p;
+  p.r_first = p.nd = p.seg_start = 0;
+  p.hh = p.npc = 0;
+  if (bh >= static_cast<int64_t>(a.batch) * a.q_heads) return p;
   const int b = static_cast<int>(bh / a.q_heads);
   const int hq = static_cast<int>(bh - static_cast<int64_t>(b) * a.q_heads);
   const int tb = a.hdr[0];
-  RangeMap rm;
+  RangeMap& rm = p.rm;
   rm.Pst = a.hdr[1];
   rm.C = a.hdr[2];
   rm.nwarps = a.hdr[3];
@@ -157,7 +192,7 @@ __device__ __forceinline__ void combine_row(const DecodeArgs& a, int64_t bh, int
   const int nblk = cum[b + 1] - cum[b];
   const int skip = a.skip != nullptr ? a.skip[b] : 0;
   const int npc = skip > 0 ? (skip + a.pchunk - 1) / a.pchunk : 0;
-  if (nblk == 0 && npc == 0) return;  // zeroed by the decode kernel
+  if (nblk == 0 && npc == 0) return p;  // zeroed by the decode kernel
   int hgi, hh;  // the row's q-head group in the stream, and its record row in the group
   if (a.cta_heads > 0) {  // grouped-query kernel: groups of cta_heads kv heads
     const int qpg = a.cta_heads * a.group;
@@ -169,14 +204,40 @@ __device__ __forceinline__ void combine_row(const DecodeArgs& a, int64_t bh, int
     hh = within % kHeadsPerGroup;
   }
   const int64_t seg_start = static_cast<int64_t>(hgi) * tb + cum[b];
-  int64_t r_first = 0, nd = 0;
+  p.hh = hh;
+  p.seg_start = seg_start;
   if (nblk > 0) {
-    r_first = range_of(rm, seg_start);
+    p.r_first = range_of(rm, seg_start);
     const int64_t r_last = range_of(rm, seg_start + nblk - 1);
-    if (r_first == r_last) return;  // one range: written by the decode kernel
-    nd = r_last - r_first + 1;
+    if (p.r_first == r_last) return p;  // one range: written by the decode kernel
+    p.nd = r_last - p.r_first + 1;
   }
-  merge_pieces<QBF>(a, bh, hh, lane, r_first, nd, seg_start, rm, npc);
+  p.npc = npc;
+  return p;
+}
+
+template <bool QBF>
+__device__ __forceinline__ void combine_row(const DecodeArgs& a, int64_t bh, int lane) {
+  const Pieces p = pieces_of(a, bh);
+  if (p.nd + p.npc > 0)
+    merge_pieces<QBF>(a, bh, p.hh, lane, p.r_first, p.nd, p.seg_start, p.rm, p.npc);
+}
+
+// One CTA of kWideWarps warps for each row. A row of a 100K-token request has
+// over a hundred pieces, and with few rows one warp's rounds of loads were
+// most of the merge: 128 rows of about 150 pieces took 27 us with a warp each
+// and WIDEUS us so.
+constexpr int kWideWarps = 8;
+
+template <bool QBF>
+__global__ void __launch_bounds__(32 * kWideWarps)
+    combine_wide_kernel(const __grid_constant__ DecodeArgs a) {
+  __shared__ __align__(16) float sh[kWideWarps][kPartStride];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Pieces p = pieces_of(a, blockIdx.x);
+  if (p.nd + p.npc > 0)  // (the same for the whole CTA)
+    merge_pieces<QBF, kWideWarps>(a, blockIdx.x, p.hh, threadIdx.x & 31, p.r_first, p.nd,
+                                  p.seg_start, p.rm, p.npc, threadIdx.x >> 5, sh);
 }
 
 // Launched as a programmatic dependent of the decode kernel: its CTAs may
@@ -437,6 +498,22 @@ cudaError_t launch_combine(const DecodeArgs& a, int q_dtype, cudaStream_t s) {
   cfg.numAttrs = 1;
   return q_dtype == kBF16 ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, a)
                           : cudaLaunchKernelEx(&cfg, combine_kernel<false>, a);
+}
+
+cudaError_t launch_combine_wide(const DecodeArgs& a, int q_dtype, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(a.batch) * a.q_heads;
+  if (rows == 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows));
+  cfg.blockDim = dim3(32 * kWideWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_combine
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return q_dtype == kBF16 ? cudaLaunchKernelEx(&cfg, combine_wide_kernel<true>, a)
+                          : cudaLaunchKernelEx(&cfg, combine_wide_kernel<false>, a);
 }
 
 cudaError_t launch_step(const StepArgs& a, int kv_dtype, int q_dtype, int grid,

@@ -12,6 +12,14 @@
 
 namespace kvq {
 
+// One block of the stream for each lane: its pool block, q-head group and (FP8
+// pools) scale bytes.
+struct Window {
+  int32_t phys;
+  int hgi;
+  uint32_t ke, ve;
+};
+
 // The decode of CTA `cta` out of `ncta` (the persistent grid); dsmem is the
 // CTA's dynamic shared memory, warp_sum 4 ints of static shared memory.
 // TAIL: the instantiation that can hand out tail chunks (make_range_map);
@@ -32,6 +40,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
   constexpr bool kQuant = KvTraits<KV>::kQuant;
   constexpr bool kPvBf = KV == kBF16;  // P.V product type: bf16 only for bf16 pools
   constexpr bool kF8Pool = KV == kF8;
+  constexpr bool kAhead = kF8Pool || SC;  // block ids and scales loaded windows ahead
   constexpr bool kQkBf = QBF && !kF8Pool;  // Q.K product type: FP8 pools take fp16 always
   constexpr float kAk = CodeOffset<KV, QBF>::kK;
   constexpr float kAv = CodeOffset<KV, QBF>::kV;
@@ -76,50 +85,95 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
     Cursor ic;
     locate(ic, x0, cum, a.batch, tb);
     Cursor cc = ic;  // compute side
-    int win_b = -1, win_j0 = 0, win_hgi = -1;
+    int win_b = -1, win_j0 = 0;
     int32_t win = -1;
-    // FP8 pools: K and V scale bytes of the window's blocks, one per lane, and
-    // of the blocks in flight (stage s in lane s)
-    uint32_t win_se = 0u, ring_se = 0u;
+    // FP8 and scored kernels: windows of 32 blocks of the range (whatever
+    // requests they belong to), a block a lane, loaded ahead: while one is
+    // issued the next has its ids and its scale bytes are on the way, and so
+    // are the ids of the one after it. Waiting for each window's ids and then
+    // its scales once per 32 blocks cost 4 % on long contexts; loading a
+    // block's scales as it was issued cost 20 % (the next use of the register
+    // waits for the load of the newest block).
+    Window w0, w1, w2;
+    uint32_t ring_se = 0u;  // FP8 pools: scale bytes of the blocks in flight, stage s in lane s
+    auto load_ids = [&](int first) -> Window {
+      Window w;
+      w.phys = -1;
+      w.hgi = 0;
+      w.ke = w.ve = 0u;
+      if (first + lane < n) {
+        Cursor c;
+        locate(c, x0 + first + lane, cum, a.batch, tb);
+        w.hgi = c.hgi;
+        w.phys = __ldg(a.block_tables + static_cast<int64_t>(c.b) * a.max_blocks +
+                       lead_of<SC>(a, c.b) + c.j);
+      }
+      return w;
+    };
+    auto load_scales = [&](Window& w) {
+      if constexpr (kF8Pool) {
+        if (w.phys >= 0 && w.phys < a.num_blocks) {
+          const int64_t e = static_cast<int64_t>(w.phys) * a.kv_heads + w.hgi / a.head_groups;
+          w.ke = __ldg(a.k_se + e);
+          w.ve = __ldg(a.v_se + e);
+        }
+      }
+    };
+    if constexpr (kAhead) {
+      w0 = load_ids(0);
+      w1 = load_ids(32);
+      w2 = w1;
+      load_scales(w0);
+    }
     uint32_t ok_mask = 0;  // stages holding a valid block in flight
     int k_issue = 0;   // next block of the range to issue
     int st_issue = 0;  // its stage
     auto issue_next = [&]() {
       if (k_issue < n) {
+        int32_t phys;
+        int h;
+        if constexpr (kAhead) {
+          const int kk = k_issue & 31;
+          if (kk == 0) {
+            if (k_issue > 0) {
+              w0 = w1;
+              w1 = w2;
+            }
+            load_scales(w1);
+            w2 = load_ids(k_issue + 64);
+          }
+          phys = __shfl_sync(kFull, w0.phys, kk);
+          h = __shfl_sync(kFull, w0.hgi, kk) / a.head_groups;
+        } else {
         // (a range that crosses into the next q-head group of a lone request
         // starts over at its first block)
-        if (ic.b != win_b || ic.j < win_j0 || ic.j >= win_j0 + 32 ||
-            (kF8Pool && ic.hgi != win_hgi)) {
+        if (ic.b != win_b || ic.j < win_j0 || ic.j >= win_j0 + 32) {
           win_b = ic.b;
           win_j0 = ic.j;
           const int jj = win_j0 + lane;
           win = jj < ic.nblk ? a.block_tables[static_cast<int64_t>(ic.b) * a.max_blocks +
                                               lead_of<SC>(a, ic.b) + jj]
                              : -1;
-          if constexpr (kF8Pool) {
-            win_hgi = ic.hgi;
-            win_se = 0u;
-            if (win >= 0 && win < a.num_blocks) {
-              const int64_t e = static_cast<int64_t>(win) * a.kv_heads + ic.hgi / a.head_groups;
-              win_se = a.k_se[e] | static_cast<uint32_t>(a.v_se[e]) << 8;
-            }
-          }
         }
-        const int32_t phys = __shfl_sync(kFull, win, ic.j - win_j0);
+        phys = __shfl_sync(kFull, win, ic.j - win_j0);
+        h = ic.hgi / a.head_groups;
+        }
         const bool ok = phys >= 0 && phys < a.num_blocks;
         const uint32_t bit = 1u << st_issue;
-        if constexpr (kF8Pool) {
-          const uint32_t se = __shfl_sync(kFull, win_se, ic.j - win_j0);
-          if (lane == st_issue) ring_se = se;
-        }
         if (ok) {
-          issue_block<KV>(wr, st_issue, a, lm, phys, ic.hgi / a.head_groups, lane);
+          issue_block<KV>(wr, st_issue, a, lm, phys, h, lane);
           ok_mask |= bit;
         } else {
           ok_mask &= ~bit;
           if (lane == 0) report(a.dev_err, KVQ_DEV_ERR_BLOCK_ID);
         }
-        if (k_issue + 1 < n) advance(ic, cum, a.batch);
+        if constexpr (kF8Pool) {
+          const uint32_t se = __shfl_sync(kFull, w0.ke | w0.ve << 8, k_issue & 31);
+          if (lane == st_issue) ring_se = se;
+        }
+        if constexpr (!kAhead) {
+          if (k_issue + 1 < n) advance(ic, cum, a.batch);
+        }
       }
       if constexpr (!S::kTma) cp_async_commit();
       ++k_issue;
@@ -481,6 +535,17 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, unsigned char* 
     return true;
   };  // run_range
 
+  if constexpr (kF8Pool || SC) {
+    if (a.whole) {  // a warp for each (q-head group, request): nothing to merge
+      if (gw < static_cast<int64_t>(sp.groups) * a.batch) {
+        const int hgi = static_cast<int>(gw / a.batch);
+        const int b = static_cast<int>(gw - static_cast<int64_t>(hgi) * a.batch);
+        const int nblk = cum[b + 1] - cum[b];
+        if (nblk > 0) run_range(static_cast<int64_t>(hgi) * tb + cum[b], nblk, 0);
+      }
+      return;
+    }
+  }
   for_each_range<TAIL>(a, sp, gw, lane, run_range);
 }
 

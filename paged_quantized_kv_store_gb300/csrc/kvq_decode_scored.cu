@@ -24,6 +24,12 @@ __global__ void __launch_bounds__(kDecodeThreads, KV == kI4 ? 1 : 3)
   __shared__ int32_t warp_sum[kWarps];
   // the combine kernel may be scheduled now; it waits for this grid to finish
   asm volatile("griddepcontrol.launch_dependents;");
+  if constexpr (Stage<KV>::kTma) {
+    if (threadIdx.x == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.k_map)));
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.v_map)));
+    }
+  }
   decode_body<KV, QBF, true, SC>(a, dsmem, warp_sum, blockIdx.x, gridDim.x);
 }
 

@@ -112,6 +112,9 @@ struct DecodeArgs {
   const uint8_t* k_se;
   const uint8_t* v_se;
   ScoreArgs score;  // scored kernels only
+  // FP8 and scored kernels: a warp takes a whole (q-head group, request), and
+  // no combine kernel follows
+  bool whole;
 };
 
 struct CopyArgs {
@@ -208,6 +211,9 @@ cudaError_t launch_tables(const TablesArgs& a, cudaStream_t s);
 cudaError_t launch_decode(const DecodeArgs& a, int kv_dtype, int q_dtype, int grid_ctas,
                           cudaStream_t s);
 cudaError_t launch_combine(const DecodeArgs& a, int q_dtype, cudaStream_t s);
+// the same with kWideWarps warps for each (request, q head): few rows of many
+// pieces
+cudaError_t launch_combine_wide(const DecodeArgs& a, int q_dtype, cudaStream_t s);
 cudaError_t launch_prefix(const DecodeArgs& a, int kv_dtype, int q_dtype, int grid_ctas,
                           cudaStream_t s);
 
