@@ -20,10 +20,7 @@ namespace {
 
 constexpr int kAutoMinBlocksPerWarp = 4;  // a warp's range is never shorter than this
 constexpr float kMinSoftcap = 1e-6f, kMaxSoftcap = 1e6f;
-#ifndef WHOLE
-#define WHOLE 256
-#endif
-constexpr int kWholeTokens = WHOLE;  // longest context a warp attends alone
+constexpr int kWholeTokens = 112;  // longest context a warp attends alone
 constexpr int kWideRows = 8;  // rows for each SM up to which a CTA merges each
 
 // Decode workspace: [256 bytes: the tail-chunk counter, the fused step's

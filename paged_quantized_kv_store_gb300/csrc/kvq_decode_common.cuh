@@ -200,10 +200,14 @@ __device__ __forceinline__ StreamPlan plan_stream(const DecodeArgs& a, unsigned 
       a.hdr[4] = sp.rm.k;
     }
     for (int b = tid; b <= a.batch; b += nt) a.hdr[kHdrCum + b] = cum[b];
-    for (int b = 0; b < a.batch; ++b) {
+    // a thread for each empty request: with the whole CTA looking at one
+    // request after the other, CTA 0 began its ranges 12 us after the others
+    // in a batch of 256
+    for (int b = tid; b < a.batch; b += nt) {
       if (cum[b + 1] != cum[b] || skip_of(a, b) > 0) continue;
-      for (int e = tid; e < a.q_heads * kHeadDim; e += nt)
-        store_out<QBF>(a.out, static_cast<int64_t>(b) * a.q_heads * kHeadDim + e, 0.f);
+      uint4* row = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                            static_cast<int64_t>(b) * a.q_heads * kHeadDim);
+      for (int e = 0; e < a.q_heads * kHeadDim / 8; ++e) row[e] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
   return sp;

@@ -211,8 +211,7 @@ cudaError_t launch_tables(const TablesArgs& a, cudaStream_t s);
 cudaError_t launch_decode(const DecodeArgs& a, int kv_dtype, int q_dtype, int grid_ctas,
                           cudaStream_t s);
 cudaError_t launch_combine(const DecodeArgs& a, int q_dtype, cudaStream_t s);
-// the same with kWideWarps warps for each (request, q head): few rows of many
-// pieces
+// the same with a CTA for each (request, q head): few rows of many pieces
 cudaError_t launch_combine_wide(const DecodeArgs& a, int q_dtype, cudaStream_t s);
 cudaError_t launch_prefix(const DecodeArgs& a, int kv_dtype, int q_dtype, int grid_ctas,
                           cudaStream_t s);
