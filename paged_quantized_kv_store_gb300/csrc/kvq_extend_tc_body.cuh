@@ -991,6 +991,12 @@ __device__ __forceinline__ void staging_role(const ExtendArgs& a, const TcShared
   }
 }
 
+// A block of the context for each lane: its id and (FP8 pools) scale bytes.
+struct BlockWin {
+  int id;
+  uint32_t ke, ve;
+};
+
 // Raw-ring producer (INT8 pools; warp 14): hands out the units, and for each
 // tile of each unit one lane writes which of the tile's four blocks are valid
 // into the next raw stage and copies, for the unit's kv head, the four
@@ -1015,20 +1021,30 @@ __device__ __forceinline__ void producer_role(const ExtendArgs& a, const TcShare
     const TcUnit w = tc_unit<SC, can_split<KV, SC>()>(a, c.ucum, u);
     const int32_t* bt = a.block_tables + static_cast<int64_t>(w.b) * a.max_blocks;
     const int tokb = w.j0 * kTcTok;
-    int4 blk = tile_blocks(bt, tokb, a.max_blocks);
-    // FP8 pools: the K and V scale bytes of block lane % 4 of a tile, loaded a
-    // tile ahead, its block ids two tiles ahead
-    int4 blk_next = blk;
-    uint32_t se = 0u;
-    auto load_se = [&](const int4& ids, int tok0) -> uint32_t {
-      uint32_t valid;
-      const int phys = pick4(safe_blocks(a, ids, tok0, w.s.L, &valid), lane & 3);
-      const int64_t e = static_cast<int64_t>(phys) * a.kv_heads + w.h;
-      return __ldg(a.k_se + e) | static_cast<uint32_t>(__ldg(a.v_se + e)) << 8;
+    int4 blk = make_int4(0, 0, 0, 0);
+    if constexpr (KV != kF8) blk = tile_blocks(bt, tokb, a.max_blocks);
+    // FP8 pools: ids and scale bytes in windows of 32 blocks (8 tiles), a block
+    // a lane: while one window is copied, the next one's ids and then its scales
+    // are on the way. (With a tile's scales loaded one tile ahead, each tile
+    // waited for a load: 1.36 us a tile whatever the other roles did.)
+    BlockWin win, nxt;
+    auto load_ids = [&](int wi) {
+      const int b = w.j0 * 4 + 32 * wi + lane;
+      BlockWin x;
+      x.id = b * kBlock < w.s.L && b < a.max_blocks ? __ldg(bt + b) : -1;
+      x.ke = x.ve = 0u;
+      return x;
+    };
+    auto load_scales = [&](BlockWin& x) {
+      if (x.id >= 0 && x.id < a.num_blocks) {
+        const int64_t e = static_cast<int64_t>(x.id) * a.kv_heads + w.h;
+        x.ke = __ldg(a.k_se + e);
+        x.ve = __ldg(a.v_se + e);
+      }
     };
     if constexpr (KV == kF8) {
-      blk_next = tile_blocks(bt, tokb + kTcTok, a.max_blocks);
-      se = load_se(blk, tokb);
+      nxt = load_ids(0);
+      load_scales(nxt);
     }
     for (int j = 0; j < w.ntiles; ++j) {
       const uint32_t rs = rt % kRawStages, use = rt / kRawStages;
@@ -1038,15 +1054,29 @@ __device__ __forceinline__ void producer_role(const ExtendArgs& a, const TcShare
         break;
       }
       uint32_t valid;
-      const int4 sb = safe_blocks(a, blk, tokb + j * kTcTok, w.s.L, &valid);
+      int4 sb;
       uint32_t ke = 0u, ve = 0u;
       if constexpr (KV == kF8) {
+        if ((j & 7) == 0) {
+          win = nxt;
+          nxt = load_ids(j / 8 + 1);
+        } else if ((j & 7) == 4) {
+          load_scales(nxt);
+        }
+        const bool there = win.id >= 0 && win.id < a.num_blocks;
+        const int first = 4 * (j & 7);
+        valid = (__ballot_sync(kFull, there) >> first) & 15u;
+        const int id = there ? win.id : 0;
+        sb = make_int4(__shfl_sync(kFull, id, first), __shfl_sync(kFull, id, first + 1),
+                       __shfl_sync(kFull, id, first + 2), __shfl_sync(kFull, id, first + 3));
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const uint32_t x = __shfl_sync(kFull, se, b);
+          const uint32_t x = __shfl_sync(kFull, win.ke | win.ve << 8, first + b);
           ke |= (x & 0xFFu) << (8 * b);
           ve |= (x >> 8) << (8 * b);
         }
+      } else {
+        sb = safe_blocks(a, blk, tokb + j * kTcTok, w.s.L, &valid);
       }
       if (lane == 0) {
         const uint32_t st = c.base + kRawOff + rs * kRawBytes, bar = c.bar(kBarRawFull + rs);
@@ -1071,13 +1101,7 @@ __device__ __forceinline__ void producer_role(const ExtendArgs& a, const TcShare
       }
       __syncwarp();
       ++rt;
-      if constexpr (KV == kF8) {
-        blk = blk_next;
-        se = load_se(blk, tokb + (j + 1) * kTcTok);
-        blk_next = tile_blocks(bt, tokb + (j + 2) * kTcTok, a.max_blocks);
-      } else {
-        blk = tile_blocks(bt, tokb + (j + 1) * kTcTok, a.max_blocks);
-      }
+      if constexpr (KV != kF8) blk = tile_blocks(bt, tokb + (j + 1) * kTcTok, a.max_blocks);
     }
   }
   if (lane == 0)
