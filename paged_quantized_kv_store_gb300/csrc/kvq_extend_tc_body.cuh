@@ -22,10 +22,12 @@ constexpr int kStageThreads = 128;        // staging warpgroup
 constexpr int kSoftWarps = 8;             // warps 0-7: softmax warpgroups 0 and 1
 constexpr int kMmaWarp = 12;              // warps 8-11 stage, warps 12 and 13 issue the MMAs
 constexpr int kTcThreads = 16 * 32;       // four warpgroups; warp 14 copies the raw codes of
-                                          // INT8 pools, warp 15 only holds registers
+                                          // INT8 and FP8 pools, warp 15 only holds registers
 // Registers per thread after the split (setmaxnreg): the launch gives every
 // thread 65536 / 512 = 128; the staging and MMA warpgroups give theirs back
-// down to kLowRegs, the softmax warpgroups take them up to kHighRegs.
+// down to kLowRegs, the softmax warpgroups take them up to kHighRegs. (FP8
+// pools with a second staging warpgroup, 640 threads and 96 registers at
+// launch: 170 us instead of 155 for a 4096-token prompt with 32/8 heads.)
 constexpr uint32_t kLowRegs = 120, kHighRegs = 136;
 static_assert(2 * kLowRegs + 2 * kHighRegs == 4 * (65536 / kTcThreads),
               "the split must add up to the launch's registers");
@@ -67,17 +69,21 @@ template <int KV>
 constexpr uint32_t raw_tx() {  // bytes the copies of a stage bring
   return 8 * kRawBox + (KV == kI8 ? 2 * kTcTok * 4 : 0);
 }
-constexpr uint32_t kRawBytes = (kRawValidOff + 16 + 1023) / 1024 * 1024;
+constexpr uint32_t kRawBytes = (kRawValidOff + 64 + 1023) / 1024 * 1024;
 constexpr uint32_t kRawOff = (kInfoOff + kStages * 16 + 1023) / 1024 * 1024;
 template <int KV, bool SC>
 constexpr bool can_split() { return KV == kF8 || SC; }
 template <int KV>
 constexpr bool raw_ring() { return KV == kI8 || KV == kF8; }
-// FP8 pools: a raw stage's words at kRawValidOff are the valid bits, then the
-// four blocks' K scale bytes and V scale bytes; a K/V stage's scale array
-// holds, as floats, the four blocks' K factors (softmax scale folded in), the
-// factor that takes O to the tile's reference exponent, and its unit.
-constexpr uint32_t kF8Ofac = 16, kF8Unit = 20;
+// FP8 pools: what the producer derives of a tile's scales, in the raw stage from
+// kRawValidOff on: the blocks' valid bits, the blocks whose K codes and whose V
+// codes stand for something (a bit each), a pad; then, as floats, the blocks' K
+// factors (softmax scale folded in); their V factors 2^(scale - reference) as
+// fp16 pairs; the factor that takes O to the tile's reference, and its unit.
+// The staging copies the K factors and the last two on to the stage's scale
+// array, for the softmax.
+constexpr uint32_t kF8Kf = 16, kF8Vf = 32, kF8Ofac = 48;
+constexpr uint32_t kF8SzOfac = 16;
 // V scales within [kRefLow, kRefHigh] powers of two of the reference stay:
 // codes up to 448 * 2^7 and down to 2^-9 * 2^-8 are exact in fp16.
 constexpr int kRefLow = -8, kRefHigh = 7;
@@ -97,8 +103,9 @@ constexpr uint32_t kBarRawFull = kBarDrain + 1;     // raw stage landed (TMA byt
 constexpr uint32_t kBarRawEmpty = kBarRawFull + kRawStages;  // raw stage read (128 arrivals)
 constexpr uint32_t kNumBars = kBarRawEmpty + kRawStages;
 constexpr uint32_t kSlotOff = kBarOff + 8 * kNumBars;  // TMEM base address
+constexpr uint32_t kUnitWords = 12;                    // a unit as publish_unit writes it
 constexpr uint32_t kUnitOff = kSlotOff + 4;            // 2 unit slots
-constexpr uint32_t kAbortOff = kUnitOff + 8;
+constexpr uint32_t kAbortOff = kUnitOff + 2 * 4 * kUnitWords;
 constexpr uint32_t kFixedBytes = kAbortOff + 4;
 // requests per launch (their unit prefix sums live in shared memory)
 constexpr int kTcMaxBatch = 4096;
@@ -352,31 +359,30 @@ __device__ __forceinline__ void load_tile(const ExtendArgs& a, const StageMap<KV
   }
 }
 
-// The same registers as load_tile, for an INT8 or FP8 pool, read from raw stage
+// The same registers as load_tile, for an INT8 pool, read from raw stage
 // `st` (shared address) where the copies of tile tok0 have landed: row t of
 // the K and V regions is tile token t, its 16-byte chunk c at c ^ (t mod 8).
-template <int KV, bool EX>
+template <bool EX>
 __device__ __forceinline__ void read_tile(const ExtendArgs& a, uint32_t st, int tok0, int L,
-                                          int tid, RawTile<KV>& r) {
-  using R = RawTile<KV>;
-  constexpr bool kWords = KV == kI8;  // a scale/zero word for each token
+                                          int tid, RawTile<kI8>& r) {
+  using R = RawTile<kI8>;
   const uint32_t valid = lds32(st + kRawValidOff);
   r.kmask = 0u;
 #pragma unroll
   for (int i = 0; i < R::kKChunks; ++i) {
     int t, ch;
-    k_item<KV>(tid + kStageThreads * i, t, ch);
+    k_item<kI8>(tid + kStageThreads * i, t, ch);
     r.k[i] = lds128(st + t * 128 + ((ch ^ (t & 7)) << 4));
     r.kmask |= ((valid >> (t / kBlock)) & 1u && tok0 + t < L ? 1u : 0u) << i;
-    if constexpr (kWords && !EX) r.ksz4[i] = lds32(st + kRawSzOff + 4 * t);
+    if constexpr (!EX) r.ksz4[i] = lds32(st + kRawSzOff + 4 * t);
   }
   int tg, dc;
-  v_item<KV>(tid, tg, dc);
+  v_item<kI8>(tid, tg, dc);
   const bool vok = (valid >> (tg >> 1)) & 1u;  // tokens 8 tg .. 8 tg + 7: block tg / 2
   r.vmask = 0u;
 #pragma unroll
   for (int t = 0; t < 8; ++t) r.vmask |= (vok && tok0 + 8 * tg + t < L ? 1u : 0u) << t;
-  if constexpr (kWords && !EX) {
+  if constexpr (!EX) {
     const uint4 w0 = lds128(st + kRawSzOff + 4 * kTcTok + 32 * tg);
     const uint4 w1 = lds128(st + kRawSzOff + 4 * kTcTok + 32 * tg + 16);
     r.vsz8[0] = w0.x; r.vsz8[1] = w0.y; r.vsz8[2] = w0.z; r.vsz8[3] = w0.w;
@@ -397,7 +403,7 @@ __device__ __forceinline__ void read_tile(const ExtendArgs& a, uint32_t st, int 
     const bool ok = (valid >> (tid / kBlock)) & 1u;
     r.sz_ok = ok && tok0 + tid < L;
     r.miss = tok0 + tid < L && !ok;
-    if constexpr (kWords && EX) {
+    if constexpr (EX) {
       r.ksz = lds32(st + kRawSzOff + 4 * tid);
       r.vsz = lds32(st + kRawSzOff + 4 * kTcTok + 4 * tid);
     }
@@ -425,61 +431,9 @@ __device__ __forceinline__ uint32_t piece_pair(const uint32_t (&w)[RawTile<KV>::
 // of each half-tile and the two 32-token masks of missing tokens. `tid` is
 // the staging thread (0..127).
 // fp16 pair (mid, mid) of a pool kind: 128 for INT8 codes, 8 for INT4
-// An FP8 tile's scales as its staging threads derive them: the blocks whose K
-// and V codes stand for something (a bit each), each block's V factor
-// 2^(scale - reference) as an fp16 pair, and what the softmax reads of it.
-struct F8Tile {
-  uint32_t k_live = 0u, v_live = 0u;
-  uint32_t vf2[4] = {0u, 0u, 0u, 0u};
-  float kf[4] = {0.f, 0.f, 0.f, 0.f};
-  float ofac = 1.f, unit = 0.f;
-};
-
-// The tile's scales from its raw stage at `st`; vref: the unit's reference
-// scale byte, moved when the tile's V scales leave its range (O is then
-// rescaled by ofac before the tile's product is added).
-__device__ __forceinline__ F8Tile f8_tile(const ExtendArgs& a, uint32_t st, uint32_t& vref) {
-  F8Tile f;
-  const uint32_t valid = lds32(st + kRawValidOff), ke = lds32(st + kRawValidOff + 4),
-                 ve = lds32(st + kRawValidOff + 8);
-  int top = 0;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const uint32_t k8 = (ke >> (8 * b)) & 0xFFu, v8 = (ve >> (8 * b)) & 0xFFu;
-    const bool ok = (valid >> b) & 1u;
-    f.k_live |= (ok && k8 != 0u ? 1u : 0u) << b;
-    f.v_live |= (ok && v8 != 0u ? 1u : 0u) << b;
-    // (codes that stand for zeros are staged as zeros: any factor serves)
-    f.kf[b] = a.sm_scale_log2 * (k8 != 0u ? fp8_scale(k8) : 1.f);
-    if (ok) top = max(top, static_cast<int>(v8));
-  }
-  if (top != 0) {
-    const int d = top - static_cast<int>(vref);
-    if (vref == 0u) {  // nothing but zeros so far
-      vref = top;
-    } else if (d > kRefHigh || (d < kRefLow && d >= -90)) {
-      f.ofac = d > 126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 - d) << 23);
-      vref = top;
-    }
-  }
-  f.unit = fp8_scale(vref);
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const int d = static_cast<int>((ve >> (8 * b)) & 0xFFu) - static_cast<int>(vref);
-    const float x = d < -24 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + min(d, 15)) << 23);
-    f.vf2[b] = pack2<false>(x, x);
-  }
-  return f;
-}
-
 template <int KV>
 __device__ __forceinline__ uint32_t kMidPair() {
   return KV == kI8 ? 0x58005800u : 0x48004800u;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
 }
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
@@ -487,12 +441,9 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   return d;
 }
 
-// FP8 pools: kf and vf are the four blocks' K factors (0: the block's codes
-// stand for zeros) and V factors.
 template <int KV, bool QBF, bool EX, bool SC>
 __device__ __forceinline__ void store_tile(const ExtendArgs& a, const RawTile<KV>& r, uint32_t kt,
-                                           uint32_t vt, uint32_t sz, uint32_t info, int tid,
-                                           const F8Tile& f8 = F8Tile()) {
+                                           uint32_t vt, uint32_t sz, uint32_t info, int tid) {
   using R = RawTile<KV>;
   constexpr int kMid = KV == kI8 ? 128 : 8;
   constexpr bool VDEQ = !EX;  // K and V are staged dequantized
@@ -514,14 +465,6 @@ __device__ __forceinline__ void store_tile(const ExtendArgs& a, const RawTile<KV
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
     if ((tid & 31) == 0) sts32(info + 4 * (tid >> 5), __float_as_uint(mx));
-  }
-  if constexpr (KV == kF8) {
-    if (tid == 0) {
-      sts128(sz, __float_as_uint(f8.kf[0]), __float_as_uint(f8.kf[1]), __float_as_uint(f8.kf[2]),
-             __float_as_uint(f8.kf[3]));
-      sts32(sz + kF8Ofac, __float_as_uint(f8.ofac));
-      sts32(sz + kF8Unit, __float_as_uint(f8.unit));
-    }
   }
   if (tid < kTcTok) {
     const uint32_t miss = __ballot_sync(kFull, r.miss);
@@ -546,14 +489,6 @@ __device__ __forceinline__ void store_tile(const ExtendArgs& a, const RawTile<KV
     };
     if constexpr (KV == kF16) {
       sts128(kt + umma_kmajor_offset(kTcTok, t, 8 * ch), x[0], x[1], x[2], x[3]);
-    } else if constexpr (KV == kF8) {  // the codes' values; the softmax applies the scale
-      const bool live = (r.kmask >> i) & (f8.k_live >> (t / kBlock)) & 1u;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const uint32_t w0 = live ? x[2 * hf] : 0u, w1 = live ? x[2 * hf + 1] : 0u;
-        sts128(kt + umma_kmajor_offset(kTcTok, t, 16 * ch + 8 * hf), e4m3_lo_to_f16(w0),
-               e4m3_hi_to_f16(w0), e4m3_lo_to_f16(w1), e4m3_hi_to_f16(w1));
-      }
     } else if constexpr (KV == kI8) {
       // c - 128 exactly: fp16 by a byte permute into 1024 + c and one packed
       // subtract; bf16 through fp32
@@ -590,17 +525,6 @@ __device__ __forceinline__ void store_tile(const ExtendArgs& a, const RawTile<KV
   // dequantized V (fp16 queries): per token pair, (S, S') and (Z + mid S, ..)
   // as fp16 pairs, zero for tokens outside the context
   uint32_t s2[4], z2[4];
-  // FP8 pools: the block's factor, and the byte pairs of tokens to keep
-  uint32_t vf2 = 0u, vkeep[4];
-  if constexpr (KV == kF8) {
-    const int vb = tg >> 1;  // tokens 8 tg .. 8 tg + 7: block tg / 2
-    vf2 = vb == 0 ? f8.vf2[0] : vb == 1 ? f8.vf2[1] : vb == 2 ? f8.vf2[2] : f8.vf2[3];
-    const uint32_t m = (f8.v_live >> vb) & 1u ? r.vmask : 0u;
-#pragma unroll
-    for (int tp = 0; tp < 4; ++tp)
-      vkeep[tp] = ((m >> (2 * tp)) & 1u ? 0x00FF00FFu : 0u) |
-                  ((m >> (2 * tp + 1)) & 1u ? 0xFF00FF00u : 0u);
-  }
   if constexpr (VDEQ && KvTraits<KV>::kQuant) {
 #pragma unroll
     for (int tp = 0; tp < 4; ++tp) {
@@ -623,11 +547,6 @@ __device__ __forceinline__ void store_tile(const ExtendArgs& a, const RawTile<KV
                                  (q & 1) ? 0x7362u : 0x5140u);
         lo[tp] = bytes_to_f16(tb, 0x4140u);
         hi[tp] = bytes_to_f16(tb, 0x4342u);
-      } else if constexpr (KV == kF8) {  // transposed likewise; code * 2^(scale - reference)
-        const uint32_t tb = prmt(r.v[2 * tp][q >> 1], r.v[2 * tp + 1][q >> 1],
-                                 (q & 1) ? 0x7362u : 0x5140u) & vkeep[tp];
-        lo[tp] = hmul2(e4m3_lo_to_f16(tb), vf2);
-        hi[tp] = hmul2(e4m3_hi_to_f16(tb), vf2);
       } else {
         uint32_t p0 = piece_pair<KV>(r.v[2 * tp], q);
         uint32_t p1 = piece_pair<KV>(r.v[2 * tp + 1], q);
@@ -645,6 +564,126 @@ __device__ __forceinline__ void store_tile(const ExtendArgs& a, const RawTile<KV
     }
     sts128(vt + umma_kmajor_offset(kVRows, 8 * dc + 2 * q, 8 * tg), lo[0], lo[1], lo[2], lo[3]);
     sts128(vt + umma_kmajor_offset(kVRows, 8 * dc + 2 * q + 1, 8 * tg), hi[0], hi[1], hi[2], hi[3]);
+  }
+}
+
+// ---- FP8 pools ------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// A tile's scales from its blocks' K and V scale bytes (a byte each): written
+// by one thread to the words `st` of the raw stage. vref: the unit's reference
+// scale byte, moved when the tile's V scales leave its range (O is then
+// rescaled before the tile's product is added). qk: the softmax scale.
+__device__ __forceinline__ void f8_scales(uint32_t st, uint32_t valid, uint32_t ke, uint32_t ve,
+                                          float qk, uint32_t& vref, bool write) {
+  uint32_t k_live = 0u, v_live = 0u, vf[4];
+  float kf[4], ofac = 1.f;
+  int top = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const uint32_t k8 = (ke >> (8 * b)) & 0xFFu, v8 = (ve >> (8 * b)) & 0xFFu;
+    const bool ok = (valid >> b) & 1u;
+    k_live |= (ok && k8 != 0u ? 1u : 0u) << b;
+    v_live |= (ok && v8 != 0u ? 1u : 0u) << b;
+    // (codes that stand for zeros are staged as zeros: any factor serves)
+    kf[b] = qk * (k8 != 0u ? fp8_scale(k8) : 1.f);
+    if (ok) top = max(top, static_cast<int>(v8));
+  }
+  if (top != 0) {
+    const int d = top - static_cast<int>(vref);
+    if (vref == 0u) {  // nothing but zeros so far
+      vref = top;
+    } else if (d > kRefHigh || (d < kRefLow && d >= -90)) {
+      ofac = d > 126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 - d) << 23);
+      vref = top;
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int d = static_cast<int>((ve >> (8 * b)) & 0xFFu) - static_cast<int>(vref);
+    const float x = d < -24 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + min(d, 15)) << 23);
+    vf[b] = pack2<false>(x, x);
+  }
+  if (write) {
+    sts128(st, valid, k_live, v_live, 0u);
+    sts128(st + kF8Kf, __float_as_uint(kf[0]), __float_as_uint(kf[1]), __float_as_uint(kf[2]),
+           __float_as_uint(kf[3]));
+    sts128(st + kF8Vf, vf[0], vf[1], vf[2], vf[3]);
+    sts128(st + kF8Ofac, __float_as_uint(ofac), __float_as_uint(fp8_scale(vref)), 0u, 0u);
+  }
+}
+
+// One tile from raw stage `raw` to a stage of the K/V ring: K's codes as exact
+// fp16 values, V transposed and times its block's factor. Item i of a thread's
+// K chunks is token t0 + 16 i, of block i; all tiles' addresses differ by the
+// stage's base only. Tokens from nt on lie behind the context.
+__device__ __forceinline__ void stage_f8(const ExtendArgs& a, uint32_t raw, uint32_t kt,
+                                         uint32_t vt, uint32_t sz, uint32_t info, int nt,
+                                         int tid) {
+  int t0, ch, tg, dc;
+  k_item<kF8>(tid, t0, ch);
+  v_item<kF8>(tid, tg, dc);
+  const uint4 w = lds128(raw + kRawValidOff);  // valid, live K, live V
+  uint4 k[4];
+  uint2 v[8];
+  const uint32_t kraw = raw + t0 * 128 + ((ch ^ (t0 & 7)) << 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) k[i] = lds128(kraw + 2048 * i);
+  const uint32_t vrow = raw + kRawVOff + 8 * tg * 128 + 8 * (dc & 1);
+#pragma unroll
+  for (int t = 0; t < 8; ++t) v[t] = lds64(vrow + t * 128 + (((dc >> 1) ^ t) << 4));
+  const uint32_t vf = lds32(raw + kRawValidOff + kF8Vf + 4 * (tg >> 1));
+  if (tid == 0) {
+    const uint4 kf = lds128(raw + kRawValidOff + kF8Kf), ou = lds128(raw + kRawValidOff + kF8Ofac);
+    sts128(sz, kf.x, kf.y, kf.z, kf.w);
+    sts128(sz + kF8SzOfac, ou.x, ou.y, 0u, 0u);
+  }
+  if (tid < kTcTok) {
+    const bool miss = tid < nt && ((w.x >> (tid / kBlock)) & 1u) == 0u;
+    const uint32_t m = __ballot_sync(kFull, miss);
+    if ((tid & 31) == 0) sts32(info + 8 + 4 * (tid >> 5), m);
+    if (miss) report(a.dev_err, KVQ_DEV_ERR_BLOCK_ID);
+  }
+  // chunk ch holds dims 16 ch .. 16 ch + 15: 16-byte chunks 2 (ch mod 4) and
+  // the next of column block ch / 4
+  const uint32_t kdst = kt + (ch >> 2) * (kTcTok * 128) + t0 * 128;
+  const uint32_t c0 = ((2 * (ch & 3)) ^ (t0 & 7)) << 4, c1 = ((2 * (ch & 3) + 1) ^ (t0 & 7)) << 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t live = ((w.y >> i) & 1u) != 0u && t0 + 16 * i < nt ? 0xFFFFFFFFu : 0u;
+    const uint32_t x0 = k[i].x & live, x1 = k[i].y & live, x2 = k[i].z & live, x3 = k[i].w & live;
+    sts128(kdst + 2048 * i + c0, e4m3_lo_to_f16(x0), e4m3_hi_to_f16(x0), e4m3_lo_to_f16(x1),
+           e4m3_hi_to_f16(x1));
+    sts128(kdst + 2048 * i + c1, e4m3_lo_to_f16(x2), e4m3_hi_to_f16(x2), e4m3_lo_to_f16(x3),
+           e4m3_hi_to_f16(x3));
+  }
+  // V: the tokens to keep as byte masks of [t, t + 1, t, t + 1]
+  const int left = ((w.z >> (tg >> 1)) & 1u) != 0u ? nt - 8 * tg : 0;
+  if (left < 8) {
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      if (t >= left) v[t] = make_uint2(0u, 0u);
+  }
+  const uint32_t vdst = vt + 8 * dc * 128;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int tp = 0; tp < 4; ++tp) {
+      // bytes [t0 d, t1 d, t0 d', t1 d'] of dims d = 2q, d' = 2q + 1
+      const uint32_t tb = prmt(q < 2 ? v[2 * tp].x : v[2 * tp].y,
+                               q < 2 ? v[2 * tp + 1].x : v[2 * tp + 1].y,
+                               (q & 1) ? 0x7362u : 0x5140u);
+      lo[tp] = hmul2(e4m3_lo_to_f16(tb), vf);
+      hi[tp] = hmul2(e4m3_hi_to_f16(tb), vf);
+    }
+    sts128(vdst + (2 * q) * 128 + ((tg ^ (2 * q)) << 4), lo[0], lo[1], lo[2], lo[3]);
+    sts128(vdst + (2 * q + 1) * 128 + ((tg ^ (2 * q + 1)) << 4), hi[0], hi[1], hi[2], hi[3]);
   }
 }
 
@@ -834,6 +873,7 @@ __device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f) {
 // ---- work units -----------------------------------------------------------------
 
 struct TcUnit {
+  bool live;  // false: the work has ended
   int b, h, qt, ntiles;
   int c;     // part of the context
   int j0;    // first context tile (0 without a window, in the first part)
@@ -854,6 +894,7 @@ __device__ __forceinline__ TcUnit tc_unit(const ExtendArgs& a, const int32_t* uc
     if (ucum[mid] <= u) lo = mid; else hi = mid - 1;
   }
   TcUnit w;
+  w.live = true;
   w.b = lo;
   w.s = tc_req<SPLIT>(a, lo);
   int r = u - ucum[lo];
@@ -899,17 +940,60 @@ struct TcShared {
 // ---- roles ------------------------------------------------------------------------
 
 // Hands out unit k (an atomic counter) through slot k mod 2 once every
-// working warp has read unit k - 2 from it. The one thread that runs it is
-// the raw-ring producer's lane 0 (INT8 pools: it runs furthest ahead, so the
-// copies of a unit's first tiles start while the previous unit is staged),
-// else thread 0 of the staging warpgroup.
+// working warp has read unit k - 2 from it, with what the roles want to know of
+// it: looking the request up costs a chain of loads that one thread, running
+// ahead, takes for all. That thread is the raw-ring producer's lane 0 (INT8 and
+// FP8 pools: it runs furthest ahead, so the copies of a unit's first tiles start
+// while the previous unit is staged), else thread 0 of the staging warpgroup.
+template <bool SC, bool SPLIT>
 __device__ __forceinline__ void publish_unit(const ExtendArgs& a, const TcShared& c, uint32_t k) {
   const uint32_t slot = k & 1u;
+  const int u = atomicAdd(a.counter, 1);
+  TcUnit w;
+  w.live = u < c.total;
+  if (w.live) w = tc_unit<SC, SPLIT>(a, c.ucum, u);
   if (k < 2 || wait_or_abort(c.bar(kBarUnitEmpty + slot), ((k >> 1) - 1u) & 1u, c.abort_flag,
                              a.dev_err)) {
-    c.unit_slot[slot] = atomicAdd(a.counter, 1);
+    volatile int* p = c.unit_slot + kUnitWords * slot;
+    p[0] = w.live ? 1 : 0;
+    if (w.live) {
+      p[1] = w.b;
+      p[2] = w.h;
+      p[3] = w.qt;
+      p[4] = w.c;
+      p[5] = w.j0;
+      p[6] = w.ntiles;
+      p[7] = w.plen;
+      p[8] = w.s.q0;
+      p[9] = w.s.C;
+      p[10] = w.s.L;
+      p[11] = w.s.splits;
+    }
     mbar_arrive_one(c.bar(kBarUnitFull + slot));
   }
+}
+
+// Unit k, by a whole warp: false when the work (or the CTA) has ended.
+__device__ __forceinline__ bool take_unit(const ExtendArgs& a, const TcShared& c, uint32_t k,
+                                          int lane, TcUnit& w) {
+  const uint32_t slot = k & 1u;
+  if (!warp_wait(c.bar(kBarUnitFull + slot), (k >> 1) & 1u, c.abort_flag, a.dev_err)) return false;
+  const volatile int* p = c.unit_slot + kUnitWords * slot;
+  w.live = p[0] != 0;
+  w.b = p[1];
+  w.h = p[2];
+  w.qt = p[3];
+  w.c = p[4];
+  w.j0 = p[5];
+  w.ntiles = p[6];
+  w.plen = p[7];
+  w.s.q0 = p[8];
+  w.s.C = p[9];
+  w.s.L = p[10];
+  w.s.splits = p[11];
+  __syncwarp();
+  if (lane == 0) mbar_arrive_one(c.bar(kBarUnitEmpty + slot));
+  return w.live;
 }
 
 // Staging warpgroup: fills the K/V ring (and hands out the units when there
@@ -931,44 +1015,53 @@ __device__ __forceinline__ void staging_role(const ExtendArgs& a, const TcShared
   uint32_t tc = 0;  // tiles staged so far
   uint32_t rc = 0;  // raw stages consumed so far (INT8 pools)
   for (uint32_t k = 0;; ++k) {
-    const uint32_t slot = k & 1u;
-    if (!raw_ring<KV>() && tid == 0) publish_unit(a, c, k);
+    if (!raw_ring<KV>() && tid == 0) publish_unit<SC, can_split<KV, SC>()>(a, c, k);
     __syncwarp();
-    if (!warp_wait(c.bar(kBarUnitFull + slot), (k >> 1) & 1u, c.abort_flag, a.dev_err)) return;
-    const int u = c.unit_slot[slot];
-    __syncwarp();
-    if (lane == 0) mbar_arrive_one(c.bar(kBarUnitEmpty + slot));
-    if (u >= c.total) return;
-    const TcUnit w = tc_unit<SC, can_split<KV, SC>()>(a, c.ucum, u);
+    TcUnit w;
+    if (!take_unit(a, c, k, lane, w)) return;
     const int n = w.ntiles, L = w.s.L, tokb = w.j0 * kTcTok;
-    uint32_t vref = 0u;  // FP8 pools: the unit's reference scale
+    if constexpr (KV == kF8) {
+      for (int j = 0; j < n; ++j, ++tc) {
+        const uint32_t rs = tc % kRawStages, st = tc % kStages, use = tc / kStages;
+        if (!warp_wait(c.bar(kBarRawFull + rs), (tc / kRawStages) & 1u, c.abort_flag, a.dev_err))
+          return;
+        if (use > 0 &&
+            !warp_wait(c.bar(kBarKvEmpty + st), (use - 1u) & 1u, c.abort_flag, a.dev_err))
+          return;
+        stage_f8(a, c.base + kRawOff + rs * kRawBytes, c.base + kKOff + st * kKBytes,
+                 c.base + kVOff + st * kVBytes, c.base + kSzOff + st * kSzBytes,
+                 c.base + kInfoOff + st * 16u, L - tokb - j * kTcTok, tid);
+        mbar_arrive_one(c.bar(kBarRawEmpty + rs));
+        fence_async_smem();
+        mbar_arrive_one(c.bar(kBarKvFull + st));
+      }
+      continue;
+    }
     // registers -> the next K/V stage
-    auto store_one = [&](const RawTile<KV>& r, const F8Tile& f8 = F8Tile()) {
+    auto store_one = [&](const RawTile<KV>& r) {
       const uint32_t st = tc % kStages, use = tc / kStages;
       if (use > 0 &&
           !warp_wait(c.bar(kBarKvEmpty + st), (use - 1u) & 1u, c.abort_flag, a.dev_err))
         return false;
       store_tile<KV, QBF, EX, SC>(a, r, c.base + kKOff + st * kKBytes, c.base + kVOff + st * kVBytes,
-                          c.base + kSzOff + st * kSzBytes, c.base + kInfoOff + st * 16u, tid,
-                          f8);
+                          c.base + kSzOff + st * kSzBytes, c.base + kInfoOff + st * 16u, tid);
       fence_async_smem();
       mbar_arrive_one(c.bar(kBarKvFull + st));
       ++tc;
       return true;
     };
-    if constexpr (raw_ring<KV>()) {
+    if constexpr (KV == kF8) {
+    } else if constexpr (raw_ring<KV>()) {
       // the producer warp's copies land tile j in raw stage rc mod kRawStages
       for (int j = 0; j < n; ++j) {
         const uint32_t rs = rc % kRawStages, use = rc / kRawStages;
         if (!warp_wait(c.bar(kBarRawFull + rs), use & 1u, c.abort_flag, a.dev_err)) return;
         RawTile<KV> r;
         const uint32_t raw = c.base + kRawOff + rs * kRawBytes;
-        read_tile<KV, EX>(a, raw, tokb + j * kTcTok, L, tid, r);
-        F8Tile f8;
-        if constexpr (KV == kF8) f8 = f8_tile(a, raw, vref);
+        read_tile<EX>(a, raw, tokb + j * kTcTok, L, tid, r);
         mbar_arrive_one(c.bar(kBarRawEmpty + rs));
         ++rc;
-        if (!store_one(r, f8)) return;
+        if (!store_one(r)) return;
       }
     } else {
       // tile j's codes are loaded while tile j - 1 is staged, its block ids
@@ -997,11 +1090,11 @@ struct BlockWin {
   uint32_t ke, ve;
 };
 
-// Raw-ring producer (INT8 pools; warp 14): hands out the units, and for each
-// tile of each unit one lane writes which of the tile's four blocks are valid
-// into the next raw stage and copies, for the unit's kv head, the four
-// blocks' K and V rows (one TMA box per block and tensor) and their
-// scale/zero words (64-byte bulk copies); a block past the context or
+// Raw-ring producer (INT8 and FP8 pools; warp 14): hands out the units, and for
+// each tile of each unit one lane writes which of the tile's four blocks are
+// valid into the next raw stage and copies, for the unit's kv head, the four
+// blocks' K and V rows (one TMA box per block and tensor) and, INT8 pools, their
+// scale/zero words (64-byte bulk copies; FP8 pools: f8_scales); a block past the context or
 // outside the pool is read from block 0 and masked by the consumers. Before
 // the warp leaves, every copy it issued has landed (bounded waits), so none
 // is in flight when the CTA ends.
@@ -1010,15 +1103,10 @@ __device__ __forceinline__ void producer_role(const ExtendArgs& a, const TcShare
   uint32_t rt = 0;  // tiles issued
   bool ok = true;
   for (uint32_t k = 0; ok; ++k) {
-    const uint32_t slot = k & 1u;
-    if (lane == 0) publish_unit(a, c, k);
+    if (lane == 0) publish_unit<SC, can_split<KV, SC>()>(a, c, k);
     __syncwarp();
-    if (!warp_wait(c.bar(kBarUnitFull + slot), (k >> 1) & 1u, c.abort_flag, a.dev_err)) break;
-    const int u = c.unit_slot[slot];
-    __syncwarp();
-    if (lane == 0) mbar_arrive_one(c.bar(kBarUnitEmpty + slot));
-    if (u >= c.total) break;
-    const TcUnit w = tc_unit<SC, can_split<KV, SC>()>(a, c.ucum, u);
+    TcUnit w;
+    if (!take_unit(a, c, k, lane, w)) break;
     const int32_t* bt = a.block_tables + static_cast<int64_t>(w.b) * a.max_blocks;
     const int tokb = w.j0 * kTcTok;
     int4 blk = make_int4(0, 0, 0, 0);
@@ -1026,7 +1114,7 @@ __device__ __forceinline__ void producer_role(const ExtendArgs& a, const TcShare
     // FP8 pools: ids and scale bytes in windows of 32 blocks (8 tiles), a block
     // a lane: while one window is copied, the next one's ids and then its scales
     // are on the way. (With a tile's scales loaded one tile ahead, each tile
-    // waited for a load: 1.36 us a tile whatever the other roles did.)
+    // waited for a load: 1.36 us a tile instead of 1.13, whatever the other roles did.)
     BlockWin win, nxt;
     auto load_ids = [&](int wi) {
       const int b = w.j0 * 4 + 32 * wi + lane;
@@ -1042,6 +1130,7 @@ __device__ __forceinline__ void producer_role(const ExtendArgs& a, const TcShare
         x.ve = __ldg(a.v_se + e);
       }
     };
+    uint32_t vref = 0u;  // the unit's reference scale
     if constexpr (KV == kF8) {
       nxt = load_ids(0);
       load_scales(nxt);
@@ -1075,16 +1164,14 @@ __device__ __forceinline__ void producer_role(const ExtendArgs& a, const TcShare
           ke |= (x & 0xFFu) << (8 * b);
           ve |= (x >> 8) << (8 * b);
         }
+        f8_scales(c.base + kRawOff + rs * kRawBytes + kRawValidOff, valid, ke, ve,
+                  a.sm_scale_log2, vref, lane == 0);
       } else {
         sb = safe_blocks(a, blk, tokb + j * kTcTok, w.s.L, &valid);
       }
       if (lane == 0) {
         const uint32_t st = c.base + kRawOff + rs * kRawBytes, bar = c.bar(kBarRawFull + rs);
-        sts32(st + kRawValidOff, valid);
-        if constexpr (KV == kF8) {
-          sts32(st + kRawValidOff + 4, ke);
-          sts32(st + kRawValidOff + 8, ve);
-        }
+        if constexpr (KV != kF8) sts32(st + kRawValidOff, valid);
         fence_async_smem();  // after the consumers' reads of the stage's last use
         mbar_arm(bar, raw_tx<KV>());
 #pragma unroll
@@ -1125,7 +1212,7 @@ __device__ __forceinline__ bool elect_one() {
 // elected lane issues each product and commit. The two warpgroups' products
 // need no order between them; a K/V stage is released when both MMA warps
 // have committed its products (the empty barrier takes two arrivals).
-template <bool QBF, bool EX, bool SC, bool SPLIT>
+template <bool QBF, bool EX, bool SPLIT>
 __device__ __forceinline__ void mma_role(const ExtendArgs& a, const TcShared& c, int g,
                                          int lane) {
   constexpr uint32_t idesc_s = umma_idesc_f16(QBF, kWgRows, kTcTok);
@@ -1165,13 +1252,9 @@ __device__ __forceinline__ void mma_role(const ExtendArgs& a, const TcShared& c,
   };
   uint32_t tc = 0;  // tiles issued so far
   for (uint32_t k = 0;; ++k) {
-    const uint32_t slot = k & 1u;
-    if (!wait(c.bar(kBarUnitFull + slot), (k >> 1) & 1u)) return;
-    const int u = c.unit_slot[slot];
-    __syncwarp();
-    if (lane == 0) mbar_arrive_one(c.bar(kBarUnitEmpty + slot));
-    if (u >= c.total) return;
-    const int n = tc_unit<SC, SPLIT>(a, c.ucum, u).ntiles;
+    TcUnit w;
+    if (!take_unit(a, c, k, lane, w)) return;
+    const int n = w.ntiles;
     if (!wait(c.bar(kBarQFull + g), k & 1u)) return;
     if (SPLIT && n == 0) continue;
     if (!wait(c.bar(kBarKvFull + tc % kStages), (tc / kStages) & 1u)) return;
@@ -1209,14 +1292,36 @@ __device__ __forceinline__ void softmax_role(const ExtendArgs& a, const TcShared
     return warp_wait(b, parity, c.abort_flag, a.dev_err);
   };
   uint32_t tc = 0;
-  for (uint32_t k = 0;; ++k) {
-    const uint32_t slot = k & 1u;
-    if (!wait(c.bar(kBarUnitFull + slot), (k >> 1) & 1u)) return;
-    const int u = c.unit_slot[slot];
+  // FP8 pools: a unit's Q rows are copied behind the last tile of the unit before
+  // (its S has been computed, so Q's tile is free), during its product and output
+  constexpr bool kAhead = KV == kF8;
+  // (the unit is looked at here and taken when its turn comes)
+  auto fetch_q = [&](uint32_t next) {
+    const uint32_t slot = next & 1u;
+    if (!wait(c.bar(kBarUnitFull + slot), (next >> 1) & 1u)) return;
+    const volatile int* p = c.unit_slot + kUnitWords * slot;
+    if (p[0] == 0) return;
+    const int row = p[3] * kUnitRows + g * kWgRows + i;
+    const int qi = row / a.group, hq = p[2] * a.group + row % a.group;
+    const uint4* qp = reinterpret_cast<const uint4*>(
+        static_cast<const uint16_t*>(a.q) +
+        ((static_cast<int64_t>(p[8]) + qi) * a.q_heads + hq) * kHeadDim);
+    if (qi < p[9]) {
+#pragma unroll
+      for (int ch = 0; ch < 16; ++ch)
+        cp_async16(q_tile + umma_kmajor_offset(kWgRows, i, 8 * ch), qp + ch);
+    } else {  // zeros for a padding row
+#pragma unroll
+      for (int ch = 0; ch < 16; ++ch)
+        sts128(q_tile + umma_kmajor_offset(kWgRows, i, 8 * ch), 0u, 0u, 0u, 0u);
+    }
+    cp_async_commit();
     __syncwarp();
-    if (lane == 0) mbar_arrive_one(c.bar(kBarUnitEmpty + slot));
-    if (u >= c.total) return;
-    const TcUnit w = tc_unit<SC, can_split<KV, SC>()>(a, c.ucum, u);
+  };
+  for (uint32_t k = 0;; ++k) {
+    if (kAhead && k == 0) fetch_q(0);
+    TcUnit w;
+    if (!take_unit(a, c, k, lane, w)) return;
     const int row = w.qt * kUnitRows + g * kWgRows + i;
     const int qi = row / a.group;
     const int hq = w.h * a.group + row % a.group;
@@ -1225,28 +1330,28 @@ __device__ __forceinline__ void softmax_role(const ExtendArgs& a, const TcShared
 
     // Q row of this thread into the K-major tile (zeros for a padding row)
     float qsum = 0.f, qdown = 1.f;
-    if constexpr (KV == kF8 && OBF) {
-      const uint4* qp = reinterpret_cast<const uint4*>(
-          static_cast<const uint16_t*>(a.q) +
-          ((static_cast<int64_t>(w.s.q0) + qi) * a.q_heads + hq) * kHeadDim);
-      uint32_t mx = 0u;
+    if constexpr (kAhead) {
+      cp_async_wait<0>();
+      if constexpr (OBF) {  // in place: bf16 to fp16 times a power of two (q_to_f16)
+        uint32_t mx = 0u;
 #pragma unroll 4
-      for (int ch = 0; ch < 16; ++ch) {
-        const uint4 x = valid ? qp[ch] : make_uint4(0u, 0u, 0u, 0u);
-        mx = __vmaxu2(__vmaxu2(__vmaxu2(mx, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu),
-                      __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
-      }
-      const int e = min(max(static_cast<int>(max(mx & 0xFFFFu, mx >> 16) >> 7), 16), 254);
-      const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-      qdown = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
-      auto cv = [&](uint32_t p) {
-        return pack2<false>(lo_to_float<true>(p) * up, hi_to_float<true>(p) * up);
-      };
+        for (int ch = 0; ch < 16; ++ch) {
+          const uint4 x = lds128(q_tile + umma_kmajor_offset(kWgRows, i, 8 * ch));
+          mx = __vmaxu2(__vmaxu2(__vmaxu2(mx, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu),
+                        __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+        }
+        const int e = min(max(static_cast<int>(max(mx & 0xFFFFu, mx >> 16) >> 7), 16), 254);
+        const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+        qdown = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+        auto cv = [&](uint32_t p) {
+          return pack2<false>(lo_to_float<true>(p) * up, hi_to_float<true>(p) * up);
+        };
 #pragma unroll 4
-      for (int ch = 0; ch < 16; ++ch) {
-        const uint4 x = valid ? qp[ch] : make_uint4(0u, 0u, 0u, 0u);
-        sts128(q_tile + umma_kmajor_offset(kWgRows, i, 8 * ch), cv(x.x), cv(x.y), cv(x.z),
-               cv(x.w));
+        for (int ch = 0; ch < 16; ++ch) {
+          const uint32_t at = q_tile + umma_kmajor_offset(kWgRows, i, 8 * ch);
+          const uint4 x = lds128(at);
+          sts128(at, cv(x.x), cv(x.y), cv(x.z), cv(x.w));
+        }
       }
     } else {
       const uint4* qp = reinterpret_cast<const uint4*>(
@@ -1455,6 +1560,7 @@ __device__ __forceinline__ void softmax_role(const ExtendArgs& a, const TcShared
       tc_fence_before();
       mbar_arrive_one(c.bar(kBarPFull + g));
     }
+    if constexpr (kAhead) fetch_q(k + 1);
     // output row: (O + z) / l (every lane takes part in the TMEM reads)
     if (w.ntiles > 0 && !wait(c.bar(kBarODone + g), (tc - 1u) & 1u)) return;
     tc_fence_after();
@@ -1512,7 +1618,8 @@ __device__ __forceinline__ void softmax_role(const ExtendArgs& a, const TcShared
 }
 
 template <int KV, bool QBF, bool OBF = QBF, bool SC = false, bool EX = QBF>
-__global__ void __launch_bounds__(kTcThreads, 1) extend_tc_kernel(const __grid_constant__ ExtendArgs a) {
+__global__ void __launch_bounds__(kTcThreads, 1)
+    extend_tc_kernel(const __grid_constant__ ExtendArgs a) {
   constexpr bool kSplit = can_split<KV, SC>();
   extern __shared__ __align__(1024) unsigned char dsmem[];
   __shared__ int32_t warp_sum[kTcThreads / 32];
@@ -1567,7 +1674,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) extend_tc_kernel(const __grid_c
       mbar_init_count(c.bar(kBarQFull + s), kWgRows);
       mbar_init_count(c.bar(kBarUnitFull + s), 1);
       // lane 0 of every working warp: softmax, staging, MMA (and the producer)
-      mbar_init_count(c.bar(kBarUnitEmpty + s), kSoftWarps + 4 + 2 + (raw_ring<KV>() ? 1 : 0));
+      mbar_init_count(c.bar(kBarUnitEmpty + s), kMmaWarp + 2 + (raw_ring<KV>() ? 1 : 0));
       mbar_init_count(c.bar(kBarSRead + s), kWgRows);
     }
     mbar_init_count(c.bar(kBarDrain), 2);  // one commit per MMA warp
@@ -1594,7 +1701,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) extend_tc_kernel(const __grid_c
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
     if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-      mma_role<QBF, EX, SC, kSplit>(a, c, warp - kMmaWarp, lane);
+      mma_role<QBF, EX, kSplit>(a, c, warp - kMmaWarp, lane);
       // every product either MMA warp issued completes before the TMEM is freed
       __syncwarp();
       if (elect_one()) {
@@ -1632,7 +1739,8 @@ cudaError_t launch_tc_t(const ExtendArgs& a, int grid, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     opted_in_device = dev;
   }
-  extend_tc_kernel<KV, QBF, OBF, SC, EX><<<grid, kTcThreads, tc_smem_bytes(a.batch), s>>>(a);
+  extend_tc_kernel<KV, QBF, OBF, SC, EX>
+      <<<grid, kTcThreads, tc_smem_bytes(a.batch), s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || !can_split<KV, SC>() || a.pchunk == 0) return e;
   return launch_extend_combine(a, OBF, s);
