@@ -21,7 +21,11 @@ namespace {
 constexpr int kAutoMinBlocksPerWarp = 4;  // a warp's range is never shorter than this
 constexpr float kMinSoftcap = 1e-6f, kMaxSoftcap = 1e6f;
 constexpr int kWholeTokens = 112;  // longest context a warp attends alone
-constexpr int kWideRows = 8;  // rows for each SM up to which a CTA merges each
+// rows for each SM up to which a CTA merges each (128 rows of about 150 pieces:
+// the whole call 94.5 us instead of 109 with a warp each; 512 rows of a few
+// pieces: 33.1 instead of 31.6)
+constexpr int kWideRows = 2;
+constexpr int kTcPayRows = 32;  // rows of a request from which tcgen05 pays (FP8 pools)
 
 // Decode workspace: [256 bytes: the tail-chunk counter, the fused step's
 // barrier counter][header: 4 ints + batch + 1 prefix sums][partial records:
@@ -435,26 +439,52 @@ ExtendPlan extend_plan(int batch, int total_q, int q_heads, int kv_heads, int ma
 }
 
 // The same for the tcgen05 kernels that can cut the context (FP8 pools, and
-// scores): parts of whole 64-token tiles, at least 4 of them, so that about two
-// units for each SM are at hand; at most 16 parts (the combine takes 32).
-// Measured for 7 ragged chunks over 700 to 4000 tokens (about 150 units):
-// 376 us on mma.sync, and on tcgen05 PLACEHOLDER whole and cut.
-ExtendPlan extend_tc_plan(int total_q, int q_heads, int kv_heads, int max_kv_len, int num_sms) {
+// scores): n parts of whole 64-token tiles where that is the least of
+//   ceil(units n' / SMs) (1.13 us a tile + 6 us a unit) + the combine (8 us, and
+//   its records written and read),
+// the measured costs of a unit, for calls of less than two units for each SM
+// (n' of the n parts have work under a window). A batch's shortest requests
+// are counted as its longest. FP8, 32/8 heads, us whole and cut: 8 tokens
+// over 30000 521 and 52, 1500 over 30000 1018 and 754, 4 x 64 over 4000 84 and
+// 43; 16 x 32 over 2000 49 whole and 64 in two, 7 ragged chunks over 700 to
+// 4000 86 and 107: not cut.
+ExtendPlan extend_tc_plan(int batch, int total_q, int q_heads, int kv_heads, int max_kv_len,
+                          int window, int num_sms) {
+  constexpr double kTileUs = 1.13, kUnitUs = 6.0, kCombineUs = 8.0, kBytesPerUs = 6e6;
+  constexpr int kMaxParts = 16;  // (the combine takes 32)
   ExtendPlan p;
   const int group = q_heads / kv_heads;
-  const int64_t units = static_cast<int64_t>(kv_heads) *
-                        ((static_cast<int64_t>(total_q) * group + 255) / 256);
-  const int nblk = std::max(1, (max_kv_len + kBlock - 1) / kBlock);
+  const int64_t units =
+      kv_heads *
+      std::max<int64_t>(batch, (static_cast<int64_t>(total_q) * group + 255) / 256);
+  const int tiles = std::max(1, (max_kv_len + 63) / 64);
+  auto cost = [&](int parts, int seen) {  // parts of the context; tiles a unit sees
+    const int len = (tiles + parts - 1) / parts;
+    const int busy = std::min(parts, seen < tiles ? (seen + len - 1) / len + 1 : parts);
+    const double us = static_cast<double>((units * busy + num_sms - 1) / num_sms) *
+                      (std::min(len, seen) * kTileUs + kUnitUs);
+    return parts == 1 ? us
+                      : us + kCombineUs +
+                            2.0 * total_q * q_heads * parts * kvq::kPartStride * sizeof(float) /
+                                kBytesPerUs;
+  };
+  int best = 1;
+  if (total_q > 0 && units < 2 * num_sms)
+    for (int n = 2; n <= std::min(kMaxParts, tiles); ++n)
+      if (cost(n, tiles) < cost(best, tiles)) best = n;
+  // a window leaves the cut as it is or takes it away, so that the workspace
+  // of a call without one is enough
+  if (window > 0 && best > 1) {
+    const int seen = static_cast<int>(
+        std::min<int64_t>(tiles, (static_cast<int64_t>(window) + 255 / group + 63) / 64 + 1));
+    if (cost(1, seen) <= cost(best, seen)) best = 1;
+  }
   p.pchunk = 0;
   p.max_splits = 1;
-  if (units > 0 && units < 2 * num_sms) {
-    const int want = static_cast<int>(std::min<int64_t>(16, (2 * num_sms + units - 1) / units));
-    const int chunk = std::max(16, ((nblk + want - 1) / want + 3) / 4 * 4);
-    const int splits = (nblk + chunk - 1) / chunk;
-    if (splits > 1) {
-      p.pchunk = chunk;
-      p.max_splits = splits;
-    }
+  if (best > 1) {
+    const int len = (tiles + best - 1) / best;
+    p.pchunk = len * (64 / kBlock);
+    p.max_splits = (tiles + len - 1) / len;
   }
   p.part_off = 256;
   p.total = p.part_off + (p.pchunk > 0 ? static_cast<size_t>(total_q) * q_heads * p.max_splits *
@@ -642,7 +672,7 @@ kvq_status paged_extend_attn_workspace_size(int32_t batch, int32_t total_q, int3
   const int sms = current_sm_count();
   if (sms <= 0) return KVQ_ERR_CUDA;
   *bytes = std::max(extend_plan(batch, total_q, q_heads, kv_heads, max_kv_len, sms).total,
-                    extend_tc_plan(total_q, q_heads, kv_heads, max_kv_len, sms).total);
+                    extend_tc_plan(batch, total_q, q_heads, kv_heads, max_kv_len, 0, sms).total);
   return KVQ_OK;
 }
 
@@ -682,19 +712,24 @@ static kvq_status extend_impl(const kvq_pool* pool, const kvq_score* score, cons
   // tcgen05 (256-row units) when the pool kind allows it and the batch has at
   // least one unit per SM; else 16-row tiles on mma.sync (which can also cut
   // the context of a short chunk into parts). The FP8 and scored tcgen05
-  // kernels can cut it too, so there the rows of a request count: a 256-row
-  // unit with fewer than about 96 rows in use costs more than 16-row tiles.
+  // kernels can cut it too, so there the rows of a request count (4 and 16
+  // requests, 32/8 heads, us on mma.sync and on tcgen05): FP8 with 16 rows
+  // 29 and 34, 43 and 48, with 32 rows 45 and 34, 64 and 47; scored, over a
+  // window of 1024, with 48 rows 41 and 48, 64 and 50, with 64 rows 45 and 49,
+  // 78 and 51; scored INT8 with 48 rows 66 and 61, 95 and 102, with 64 rows 74
+  // and 62, 117 and 101.
   const int group = q_heads / pool->kv_heads;
   const int64_t tc_units = static_cast<int64_t>(pool->kv_heads) *
                            ((static_cast<int64_t>(total_q) * group + 255) / 256);
   const bool tc_pays = fp8 || scored
-                           ? static_cast<int64_t>(total_q) * group >= int64_t{96} * batch
+                           ? static_cast<int64_t>(total_q) * group >= int64_t{kTcPayRows} * batch * (scored ? 2 : 1)
                            : tc_units >= sms;
   const bool use_tc = variant == KVQ_EXTEND_TCGEN05 ||
                       (variant == KVQ_EXTEND_AUTO && tc_ok && tc_pays);
   const ExtendPlan plan =
       use_tc && (fp8 || scored)
-          ? extend_tc_plan(total_q, q_heads, pool->kv_heads, max_kv_len, sms)
+          ? extend_tc_plan(batch, total_q, q_heads, pool->kv_heads, max_kv_len,
+                           scored ? score->window : 0, sms)
           : extend_plan(batch, total_q, q_heads, pool->kv_heads, max_kv_len, sms);
   if (workspace == nullptr || workspace_bytes < plan.total) return KVQ_ERR_WORKSPACE;
   kvq::ExtendArgs a;
