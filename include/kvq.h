@@ -261,8 +261,11 @@ typedef struct kvq_score {
  * paged_decode_attn_scored -- paged_decode_attn with `score` (a host pointer,
  * read during the call) applied to the scores; for pools of every kind. The
  * pages have no counterpart: layers that cap, bias or window their scores read
- * the same cache. Same plan and workspace as paged_decode_attn. Rows of the
- * last block behind the request's last token are not used, whatever they hold.
+ * the same cache. Same plan and workspace as paged_decode_attn. With a cap,
+ * slopes or a window, and over FP8 pools, rows of the last block behind the
+ * request's last token are not used, whatever they hold. A score with none of
+ * them set is paged_decode_attn (whose F16, BF16, INT8 and INT4 pools need
+ * finite rows there).
  */
 kvq_status paged_decode_attn_scored(const kvq_pool* pool, const kvq_score* score, const void* q,
                                     int32_t q_dtype, void* out, const int32_t* block_tables,
@@ -409,6 +412,7 @@ kvq_status paged_extend_attn(const kvq_pool* pool, const void* q, int32_t q_dtyp
  * read during the call) applied to the scores; for pools of every kind. Same
  * workspace as paged_extend_attn. Query i of request b then sees
  *   (t <= p or t < prefix_lens[b]) and t > p - window, of its kv_lens[b] tokens.
+ * Rows behind a request's last token: as in paged_decode_attn_scored.
  */
 kvq_status paged_extend_attn_scored(const kvq_pool* pool, const kvq_score* score, const void* q,
                                     int32_t q_dtype, void* out, const int32_t* qo_indptr,
