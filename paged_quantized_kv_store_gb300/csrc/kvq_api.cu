@@ -245,17 +245,33 @@ kvq_status decode_impl(const kvq_pool* pool, const void* q, int32_t q_dtype, voi
   if (!aligned16(out)) return KVQ_ERR_INVALID_ARG;
   kvq::DecodeArgs a;
   std::memset(&a, 0, sizeof(a));
-  // the grouped-query kernel (INT8 / INT4 pools, fp16 queries, 4 q heads per
-  // kv head) serves the plain decode; the fused step keeps the general kernel
+  // the grouped-query kernel (INT8 / INT4 pools with fp16 queries, FP8 pools; 4
+  // q heads per kv head) serves the plain decode; the fused step keeps the general kernel
   // the kernels with scores and those over FP8 pools are their own
   const bool scored = score != nullptr && (score->softcap > 0.f || score->window > 0 ||
                                            score->alibi_slopes != nullptr);
-  const bool gqa = pre == nullptr && !scored && kvq::decode_gqa_supported(pool->kv_dtype, q_dtype,
-                                                                q_heads / pool->kv_heads,
-                                                                pool->kv_heads);
+  // FP8 and scored: short contexts, few enough for a warp each: a request is not
+  // cut, and nothing is left to merge
+  int scored_per_sm = 0;
+  bool whole = false;
+  if (fp8 || scored) {
+    scored_per_sm = std::min(
+        kvq::decode_scored_ctas_per_sm(pool->kv_dtype, q_dtype, scored, batch),
+        kvq::kMaxCtasPerSm);
+    if (scored_per_sm <= 0) return KVQ_ERR_CUDA;
+    const int seen = scored && score->window > 0 && score->window < max_seq_len - kBlock
+                         ? score->window + kBlock
+                         : max_seq_len;
+    whole = num_splits == 0 && seen <= kWholeTokens &&
+            static_cast<int64_t>(batch) * pool->kv_heads * plan.head_groups <=
+                static_cast<int64_t>(plan.num_sms) * scored_per_sm * (kvq::kDecodeThreads / 32);
+  }
+  const bool gqa = pre == nullptr && !scored && !whole &&
+                   kvq::decode_gqa_supported(pool->kv_dtype, q_dtype, q_heads / pool->kv_heads,
+                                             pool->kv_heads);
   const int cta_heads = gqa ? kvq::decode_gqa_cta_heads(pool->kv_heads) : 0;
   if (gqa) {  // one copy stages a block for the CTA's kv heads
-    const int row = pool->kv_dtype == KVQ_INT8 ? kHeadDim : kHeadDim / 2;
+    const int row = pool->kv_dtype == KVQ_INT4 ? kHeadDim / 2 : kHeadDim;
     if (!encode_pool_map_heads(&a.kh_map, pool->k, pool->num_blocks, pool->kv_heads, row,
                                cta_heads) ||
         !encode_pool_map_heads(&a.vh_map, pool->v, pool->num_blocks, pool->kv_heads, row,
@@ -310,7 +326,7 @@ kvq_status decode_impl(const kvq_pool* pool, const void* q, int32_t q_dtype, voi
   if (gqa) {
     // a CTA per group of cta_heads kv heads, one range each; at most
     // kMaxCtasPerSm * 4 warps per SM, as the workspace's records assume
-    const int occ = kvq::decode_gqa_ctas_per_sm(pool->kv_dtype, batch, cta_heads, false);
+    const int occ = kvq::decode_gqa_ctas_per_sm(pool->kv_dtype, q_dtype, batch, cta_heads, false);
     const int per_sm =
         std::min(occ, kvq::kMaxCtasPerSm * (kvq::kDecodeThreads / 32) / cta_heads);
     if (per_sm <= 0) return KVQ_ERR_CUDA;
@@ -369,23 +385,12 @@ kvq_status decode_impl(const kvq_pool* pool, const void* q, int32_t q_dtype, voi
   // persistent grid: as many CTAs as fit on the device at once (the
   // workspace has partial slots for kMaxCtasPerSm per SM)
   if (gqa) {
-    if (kvq::launch_decode_gqa(a, pool->kv_dtype, gqa_grid, s) != cudaSuccess)
+    if (kvq::launch_decode_gqa(a, pool->kv_dtype, q_dtype, gqa_grid, s) != cudaSuccess)
       return KVQ_ERR_CUDA;
   } else if (fp8 || scored) {
-    const int per_sm = std::min(
-        kvq::decode_scored_ctas_per_sm(pool->kv_dtype, q_dtype, scored, batch),
-        kvq::kMaxCtasPerSm);
-    if (per_sm <= 0) return KVQ_ERR_CUDA;
-    // short contexts, few enough for a warp each: a request is not cut, and
-    // nothing is left to merge
-    const int seen = scored && score->window > 0 && score->window < max_seq_len - kBlock
-                         ? score->window + kBlock
-                         : max_seq_len;
-    a.whole = num_splits == 0 && seen <= kWholeTokens &&
-              static_cast<int64_t>(batch) * pool->kv_heads * plan.head_groups <=
-                  static_cast<int64_t>(plan.num_sms) * per_sm * (kvq::kDecodeThreads / 32);
-    if (kvq::launch_decode_scored(a, pool->kv_dtype, q_dtype, scored, plan.num_sms * per_sm, s) !=
-        cudaSuccess)
+    a.whole = whole;
+    if (kvq::launch_decode_scored(a, pool->kv_dtype, q_dtype, scored,
+                                  plan.num_sms * scored_per_sm, s) != cudaSuccess)
       return KVQ_ERR_CUDA;
   } else {
     const int per_sm = std::min(kvq::decode_ctas_per_sm(pool->kv_dtype, q_dtype, batch, tail),

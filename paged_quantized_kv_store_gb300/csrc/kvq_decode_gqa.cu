@@ -1,5 +1,6 @@
-// kvq_decode_gqa: single-token decode attention over INT8 / INT4 pools for
-// queries in fp16 with 4 q heads per kv head (grouped-query attention).
+// kvq_decode_gqa: single-token decode attention with 4 q heads per kv head
+// (grouped-query attention) over INT8 / INT4 pools for queries in fp16, and
+// over FP8 pools for queries in fp16 or bf16.
 //
 // LMDeploy article (devpress.csdn.net) §2.4: INT8/INT4 KV with a per-token,
 // per-head (scale, zero); §2.2: 16-token blocks reached through block tables;
@@ -62,10 +63,21 @@
 // below 2^8 S_v; a token whose V scale is above 240 (where 2^8 S_v could
 // leave fp16) raises the maximum as soon as it exceeds it. The result is the
 // same softmax: the maximum only bounds the exponents.
+//
+// FP8 pools. A code converts to fp16 exactly, so no offset and no sum of P' is
+// needed. The scale bytes of a window's blocks are loaded half a window before
+// its first block is staged (8 bytes for K and for V: one for each kv head) and
+// travel with the stage's position. K's scale multiplies the scores; V's enters
+// P' as 2^(scale - reference), and o is moved to another reference where a
+// block's scale leaves [-2, 7] powers of two of it (P' stays below 2^15). bf16
+// queries enter as fp16 times a power of two for each head (q_to_f16). us
+// against the general kernel, which stages one kv head's tile a copy:
+// 256 x 256-2048, 32/8 heads 110 and 120; 64 x 4096 96 and 103.
 #include <cuda_runtime.h>
 
 #include "kvq_decode_common.cuh"
 #include "kvq_device.cuh"
+#include "kvq_fp8.cuh"
 #include "kvq_internal.h"
 #include "kvq_tile.cuh"
 
@@ -82,23 +94,25 @@ constexpr float kSlack = 8.f;             // the running maximum may lag the sco
 constexpr float kSlackMaxScale = 240.f;   // ... while V scales stay below this (2^8 S_v < 2^16)
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// A stage holds one block for W kv heads: [K tiles W][V tiles W][K scale/zero
-// runs W][V scale/zero runs W][position]; stages are 1024-byte aligned (the
+// A stage holds one block for W kv heads: [K tiles W][V tiles W][INT4, INT8: K
+// scale/zero runs W, V scale/zero runs W][position; FP8: K scale bytes 8, V
+// scale bytes 8]; stages are 1024-byte aligned (the
 // swizzle pattern of a tile repeats every 512 / 1024 bytes, and every tile
 // starts on such a boundary).
 template <int KV>
 struct CtaStage {
-  static constexpr int kRow = KvTraits<KV>::kRowBytes;  // 64 (INT4) or 128 (INT8)
+  static constexpr int kRow = KvTraits<KV>::kRowBytes;  // 64 (INT4) or 128 (INT8, FP8)
   static constexpr int kTile = kBlock * kRow;           // one (block, kv head) tile
   static constexpr int kDepth = KV == kI4 ? 4 : 3;
   __host__ __device__ static constexpr int v_off(int w) { return w * kTile; }
   __host__ __device__ static constexpr int sz_off(int w) { return 2 * w * kTile; }
-  __host__ __device__ static constexpr int info_off(int w) { return 2 * w * kTile + 2 * w * 64; }
+  static constexpr int kSzRun = KV == kF8 ? 0 : 64;  // scale/zero words of a tile
+  __host__ __device__ static constexpr int info_off(int w) { return 2 * w * (kTile + kSzRun); }
   __host__ __device__ static constexpr int bytes(int w) {
-    return (info_off(w) + 16 + 1023) / 1024 * 1024;
+    return (info_off(w) + 32 + 1023) / 1024 * 1024;
   }
   __host__ __device__ static constexpr uint32_t tx_bytes(int w) {
-    return static_cast<uint32_t>(2 * w * kTile + 2 * w * 64);
+    return static_cast<uint32_t>(2 * w * (kTile + kSzRun));
   }
   // chunk c of row r sits at chunk c ^ swz(r): the TMA 128-byte swizzle for
   // 128-byte rows, the 64-byte swizzle for 64-byte rows
@@ -121,6 +135,22 @@ __host__ __device__ constexpr size_t gqa_smem_bytes(int batch, int w) {
 // and zero bytes (INT8): [w.b_lo, 0, w.b_hi, 0].
 __device__ __forceinline__ uint32_t bytes_sub(uint32_t w, uint32_t sel) {
   return prmt(w, 0u, sel);
+}
+
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+// A's two halves as an MMA operand: codes 0 and 1 (or 2 and 3) of a word.
+template <int KV>
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
+  return KV == kF8 ? e4m3_lo_to_f16(w) : bytes_sub(w, 0x4140u);
+}
+template <int KV>
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
+  return KV == kF8 ? e4m3_hi_to_f16(w) : bytes_sub(w, 0x4342u);
 }
 
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
@@ -147,12 +177,13 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity
   return true;
 }
 
-template <int KV, bool TAIL>
+template <int KV, bool QBF, bool TAIL>
 __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsmem,
                                          int32_t* warp_sum, volatile int* abort_s,
                                          int32_t* chunk_s, int cta, int ncta) {
   using S = CtaStage<KV>;
   constexpr int D = S::kDepth;
+  constexpr bool kF8Pool = KV == kF8;
   constexpr float kMid = KV == kI8 ? 128.f : 8.f;
   constexpr bool kLockstep = KV != kI4;
 
@@ -164,7 +195,7 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
   const int tau = g + 8 * tsel;  // that token's row in the block
   const bool producer = warp == 0;
 
-  const StreamPlan sp = plan_stream<false, TAIL>(a, dsmem, warp_sum, cta, ncta, kLockstep,
+  const StreamPlan sp = plan_stream<QBF, TAIL>(a, dsmem, warp_sum, cta, ncta, kLockstep,
                                                  /*own_lens=*/true, /*ranges_per_cta=*/1);
   const int32_t* cum = sp.cum;
   const int32_t* lown = sp.cum + a.batch + 1;  // tokens of request b's own blocks
@@ -198,10 +229,15 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
       vro[r] = S::v_off(W) + warp * S::kTile +
                (KV == kI4 ? S::at(rows[r], g >> 1) + 8 * (g & 1) : S::at(rows[r], g));
   }
-  const uint32_t szo = S::sz_off(W) + 64 * warp + 4 * tau;  // this lane's K (V: + 64 W) pair
+  [[maybe_unused]] const uint32_t szo =
+      S::sz_off(W) + 64 * warp + 4 * tau;  // this lane's K (V: + 64 W) pair
   const float lsc = a.sm_scale_log2;  // softmax scale x log2(e)
   const uint32_t nb32 = static_cast<uint32_t>(a.num_blocks);  // valid ids are below this
   const uint32_t tx = S::tx_bytes(W);
+  // FP8 pools: the group's 8 scale bytes can be loaded at once
+  [[maybe_unused]] const bool se_wide =
+      kF8Pool && W == 8 &&
+      ((reinterpret_cast<uintptr_t>(a.k_se) | reinterpret_cast<uintptr_t>(a.v_se)) & 7u) == 0u;
 
   // blocks staged (warp 0) and consumed (every warp) by this CTA, across its
   // ranges: stage i % D, phase parity (i / D) & 1
@@ -228,11 +264,32 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
         phys = a.block_tables[static_cast<int64_t>(lo) * a.max_blocks + skip_of(a, lo) + blk];
       }
     };
+    // FP8 pools: the scale bytes of a window's blocks for the W kv heads
+    auto load_scales = [&](int32_t phys, uint32_t key, uint2& ks, uint2& vs) {
+      ks = vs = make_uint2(0u, 0u);
+      if (static_cast<uint32_t>(phys) >= nb32) return;
+      const int64_t e = static_cast<int64_t>(phys) * a.kv_heads + static_cast<int>(key >> 16) * W;
+      if (se_wide) {
+        ks = __ldg(reinterpret_cast<const uint2*>(a.k_se + e));
+        vs = __ldg(reinterpret_cast<const uint2*>(a.v_se + e));
+        return;
+      }
+      for (int i = 0; i < W; ++i) {
+        const uint32_t kb = __ldg(a.k_se + e + i), vb = __ldg(a.v_se + e + i);
+        (i < 4 ? ks.x : ks.y) |= kb << (8 * (i & 3));
+        (i < 4 ? vs.x : vs.y) |= vb << (8 * (i & 3));
+      }
+    };
     int32_t wphys = -1, nphys = -1, wblk = 0, nblk_ = 0;
     uint32_t wkey = 0, nkey = 0;
+    [[maybe_unused]] uint2 wks, wvs, nks, nvs;
     if (producer) {
       locate_window(0, wphys, wkey, wblk);
       locate_window(1, nphys, nkey, nblk_);
+      if constexpr (kF8Pool) {
+        load_scales(wphys, wkey, wks, wvs);
+        nks = nvs = make_uint2(0u, 0u);
+      }
     }
     // warp 0 stages block kq of the range into the next stage; false when the
     // CTA stops (a wait ran out)
@@ -240,9 +297,21 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
       const int kk = kq & 31;
       if (kk == 0 && kq > 0) {  // next window; locate the one after it
         wphys = nphys; wkey = nkey; wblk = nblk_;
+        if constexpr (kF8Pool) {
+          wks = nks;
+          wvs = nvs;
+        }
         locate_window((kq >> 5) + 1, nphys, nkey, nblk_);
       }
+      if constexpr (kF8Pool) {  // the next window's ids have long arrived
+        if (kk == 16) load_scales(nphys, nkey, nks, nvs);
+      }
       const int32_t phys = __shfl_sync(kFull, wphys, kk);
+      [[maybe_unused]] uint2 ks, vs;
+      if constexpr (kF8Pool) {
+        ks = make_uint2(__shfl_sync(kFull, wks.x, kk), __shfl_sync(kFull, wks.y, kk));
+        vs = make_uint2(__shfl_sync(kFull, wvs.x, kk), __shfl_sync(kFull, wvs.y, kk));
+      }
       const uint32_t key = __shfl_sync(kFull, wkey, kk);
       const int32_t blk = __shfl_sync(kFull, wblk, kk);
       const uint32_t s = n_staged % D;
@@ -258,15 +327,21 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
         } else {
           const bool ok = static_cast<uint32_t>(phys) < nb32;
           sts64(st + S::info_off(W), key, ok ? static_cast<uint32_t>(blk) : 0xFFFFFFFFu);
+          if constexpr (kF8Pool) {
+            sts64(st + S::info_off(W) + 8, ks.x, ks.y);
+            sts64(st + S::info_off(W) + 16, vs.x, vs.y);
+          }
           if (ok) {
             const int h0 = static_cast<int>(key >> 16) * W;  // first kv head of the group
-            const int64_t szi = (static_cast<int64_t>(phys) * a.kv_heads + h0) * kBlock;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arm(full, tx);
             tma_tile_4d(st, &a.kh_map, 0, 0, h0, phys, full);
             tma_tile_4d(st + S::v_off(W), &a.vh_map, 0, 0, h0, phys, full);
-            bulk_copy(st + S::sz_off(W), a.k_sz + szi, 64 * W, full);
-            bulk_copy(st + S::sz_off(W) + 64 * W, a.v_sz + szi, 64 * W, full);
+            if constexpr (!kF8Pool) {
+              const int64_t szi = (static_cast<int64_t>(phys) * a.kv_heads + h0) * kBlock;
+              bulk_copy(st + S::sz_off(W), a.k_sz + szi, 64 * W, full);
+              bulk_copy(st + S::sz_off(W) + 64 * W, a.v_sz + szi, 64 * W, full);
+            }
           } else {
             report(a.dev_err, KVQ_DEV_ERR_BLOCK_ID);
             mbar_arrive(full);  // nothing to copy: the phase completes now
@@ -286,7 +361,10 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
     const int hh0 = warp * kGqaGroup;  // this warp's first record row in the group
     int64_t seg_start = 0;
     uint32_t qb[8][2];           // Q as the B operand of S^T = K Q^T (dims permuted like K)
-    float qz0 = 0.f, qz1 = 0.f;  // sm_scale log2(e) sum(q) of this lane's two heads
+    // sm_scale log2(e) sum(q) of this lane's two heads; FP8 pools: the factors that
+    // take their products back to q's size, times sm_scale log2(e)
+    float qz0 = 0.f, qz1 = 0.f;
+    [[maybe_unused]] uint32_t vref = 0u;  // FP8 pools: scale byte o is counted in (0: none yet)
     // O^T: dims (tile i, rows g / g + 8) x columns (2t, 2t + 1); columns 0-3 take
     // tokens 0-7 of every block, columns 4-7 tokens 8-15, of heads 0-3
     float o[8][4] = {};
@@ -316,22 +394,26 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
       for (int u = 0; u < 2; ++u) {
         const int hh = 2 * t + u;
         const float l = u ? l1 : l0, m = u ? m1 : m0;
-        const float corr = (u ? z1 : z0) - kMid * R[u];
+        const float corr = kF8Pool ? 0.f : (u ? z1 : z0) - kMid * R[u];
         float acc[16];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           // INT4 output rows fed by a nibble at bits 4-7 (odd i) carry 16 c
-          const float sc = (KV == kI4 && (i & 1)) ? kTwo24 / 16.f : kTwo24;
+          const float sc = kF8Pool                    ? fp8_scale(vref)
+                           : (KV == kI4 && (i & 1)) ? kTwo24 / 16.f
+                                                    : kTwo24;
           acc[i] = fmaf(o[i][u], sc, corr);
           acc[8 + i] = fmaf(o[i][2 + u], sc, corr);
         }
         if (contained) {
           float mm = m, ll = l;
-          if (seg_skip > 0) merge_prefix(a, row0 + hh, seg_skip, g, mm, ll, acc);
+          if constexpr (!kF8Pool) {
+            if (seg_skip > 0) merge_prefix(a, row0 + hh, seg_skip, g, mm, ll, acc);
+          }
           const float inv = ll > 0.f ? 1.f / ll : 0.f;
           uint32_t w[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = pack2<false>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+          for (int i = 0; i < 8; ++i) w[i] = pack2<QBF>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
           uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
                                                 (row0 + hh) * kHeadDim + 16 * g);
           dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -388,6 +470,8 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
           const uint4 v = qp[i];
           qw[4 * i] = v.x; qw[4 * i + 1] = v.y; qw[4 * i + 2] = v.z; qw[4 * i + 3] = v.w;
         }
+        [[maybe_unused]] float down = 1.f;
+        if constexpr (kF8Pool && QBF) down = q_to_f16(qw);
         if constexpr (KV == kI4) {
           // k-step 2j: dims (8j, 8j+4) and (8j+2, 8j+6) of the lane's 32 (nibbles at
           // bits 0-3); k-step 2j + 1: (8j+1, 8j+5) and (8j+3, 8j+7) (bits 4-7)
@@ -405,13 +489,19 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
             qb[kk][1] = qw[2 * kk + 1];
           }
         }
-        float part = 0.f;
+        if constexpr (kF8Pool) {
+          qz0 = lsc * __shfl_sync(kFull, down, (2 * hp) * 4);  // lanes 4h hold head h
+          qz1 = lsc * __shfl_sync(kFull, down, (2 * hp + 1) * 4);
+          vref = 0u;
+        } else {
+          float part = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part += half_lo(qw[i]) + half_hi(qw[i]);
-        part += __shfl_xor_sync(kFull, part, 1);
-        part += __shfl_xor_sync(kFull, part, 2);  // lanes 4h hold sum(q) of head h
-        qz0 = lsc * __shfl_sync(kFull, part, (2 * hp) * 4);
-        qz1 = lsc * __shfl_sync(kFull, part, (2 * hp + 1) * 4);
+          for (int i = 0; i < 16; ++i) part += half_lo(qw[i]) + half_hi(qw[i]);
+          part += __shfl_xor_sync(kFull, part, 1);
+          part += __shfl_xor_sync(kFull, part, 2);  // lanes 4h hold sum(q) of head h
+          qz0 = lsc * __shfl_sync(kFull, part, (2 * hp) * 4);
+          qz1 = lsc * __shfl_sync(kFull, part, (2 * hp + 1) * 4);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         R[0] = R[1] = R[2] = R[3] = 0.f;
@@ -420,7 +510,14 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
       }
 
       if (blk_ok) {
-        const uint32_t ksz = lds32(st + szo), vsz = lds32(st + szo + 64 * W);
+        uint32_t ksz = 0u, vsz = 0u;  // FP8 pools: the block's scale bytes
+        if constexpr (kF8Pool) {
+          ksz = lds8(st + S::info_off(W) + 8 + warp);
+          vsz = lds8(st + S::info_off(W) + 16 + warp);
+        } else {
+          ksz = lds32(st + szo);
+          vsz = lds32(st + szo + 64 * W);
+        }
         // ---- S^T = K Q^T: class-A k-steps into sa, class-B into sb -------------------
         float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
         if constexpr (KV == kI4) {
@@ -442,12 +539,12 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
             for (int q2 = 0; q2 < 4; q2 += 2) {
               const int kk = 4 * half + q2;
               const uint32_t w0 = w4(k0, q2), w1 = w4(k1, q2);
-              const uint32_t aa[4] = {bytes_sub(w0, 0x4140u), bytes_sub(w1, 0x4140u),
-                                      bytes_sub(w0, 0x4342u), bytes_sub(w1, 0x4342u)};
+              const uint32_t aa[4] = {codes_lo<KV>(w0), codes_lo<KV>(w1), codes_hi<KV>(w0),
+                                      codes_hi<KV>(w1)};
               mma16816<false>(sa, aa, qb[kk]);
               const uint32_t v0 = w4(k0, q2 + 1), v1 = w4(k1, q2 + 1);
-              const uint32_t ab[4] = {bytes_sub(v0, 0x4140u), bytes_sub(v1, 0x4140u),
-                                      bytes_sub(v0, 0x4342u), bytes_sub(v1, 0x4342u)};
+              const uint32_t ab[4] = {codes_lo<KV>(v0), codes_lo<KV>(v1), codes_hi<KV>(v0),
+                                      codes_hi<KV>(v1)};
               mma16816<false>(sb, ab, qb[kk + 1]);
             }
           }
@@ -458,10 +555,18 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
         const float d0b = KV == kI4 ? fmaf(sb[2], 1.f / 16.f, sa[2]) : sa[2] + sb[2];
         const float d1b = KV == kI4 ? fmaf(sb[3], 1.f / 16.f, sa[3]) : sa[3] + sb[3];
         const float d0 = tsel ? d0b : d0a, d1 = tsel ? d1b : d1a;
-        const float sk = half_lo(ksz) * (kTwo24 * lsc), zk = half_hi(ksz);
-        float s0 = fmaf(sk, d0, zk * qz0), s1 = fmaf(sk, d1, zk * qz1);
+        float s0, s1;
+        if constexpr (kF8Pool) {
+          const float sk = fp8_scale(ksz);
+          s0 = ksz != 0u ? d0 * (sk * qz0) : 0.f;
+          s1 = ksz != 0u ? d1 * (sk * qz1) : 0.f;
+        } else {
+          const float sk = half_lo(ksz) * (kTwo24 * lsc), zk = half_hi(ksz);
+          s0 = fmaf(sk, d0, zk * qz0);
+          s1 = fmaf(sk, d1, zk * qz1);
+        }
         if ((j + 1) * kBlock > L && j * kBlock + tau >= L) s0 = s1 = -INFINITY;
-        const float sv = half_lo(vsz);
+        const float sv = kF8Pool ? 1.f : half_lo(vsz);
         // ---- online softmax: the running maximum moves when a score passes it by
         // more than the slack (by anything, for a token with a large V scale) ------
         const float slack = sv <= kSlackMaxScale ? kSlack : 0.f;
@@ -487,12 +592,34 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
         const float p0 = ex2(s0 - m0), p1 = ex2(s1 - m1);
         l0 += p0;
         l1 += p1;
-        const float zm = fmaf(kMid, sv, half_hi(vsz));
-        z0 = fmaf(p0, zm, z0);
-        z1 = fmaf(p1, zm, z1);
+        float pv = sv;  // what turns p into P'
+        if constexpr (kF8Pool) {
+          if (vsz != 0u) {
+            int d = static_cast<int>(vsz) - static_cast<int>(vref);
+            if (vref == 0u) {  // nothing but blocks of zeros so far
+              vref = vsz;
+              d = 0;
+            } else if (d > 7 || (d < -2 && d >= -90)) {
+              // o to the block's scale (blocks 2^90 below the reference only lose
+              // what is lost in the output's own rounding)
+              const float by = d > 126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 - d) << 23);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[i][c] *= by;
+              vref = vsz;
+              d = 0;
+            }
+            pv = d < -90 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + d) << 23);
+          }
+        } else {
+          const float zm = fmaf(kMid, sv, half_hi(vsz));
+          z0 = fmaf(p0, zm, z0);
+          z1 = fmaf(p1, zm, z1);
+        }
         // P'^T as the B operand: tokens 0-7 into columns 0-3 (lanes t = 0, 1),
         // tokens 8-15 into columns 4-7 (lanes t = 2, 3); the rest zero
-        const uint32_t hpk = pack2<false>(p0 * sv, p1 * sv);
+        const uint32_t hpk = pack2<false>(p0 * pv, p1 * pv);
         uint32_t bp[2];
         bp[0] = movmatrix_trans(tsel ? 0u : hpk);
         bp[1] = movmatrix_trans(tsel ? hpk : 0u);
@@ -527,8 +654,19 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
             }
           }
         } else {
-          const uint4 v0 = lds128(st + vro[0]), v1 = lds128(st + vro[1]);
-          const uint4 v2 = lds128(st + vro[2]), v3 = lds128(st + vro[3]);
+          uint4 v0 = lds128(st + vro[0]), v1 = lds128(st + vro[1]);
+          uint4 v2 = lds128(st + vro[2]), v3 = lds128(st + vro[3]);
+          if constexpr (kF8Pool) {
+            // codes behind the last token, and of a block of zeros, may be NaN
+            const int left = vsz != 0u ? L - j * kBlock : 0;
+            if (left < kBlock) {
+              const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+              if (2 * t >= left) v0 = none;
+              if (2 * t + 1 >= left) v1 = none;
+              if (2 * t + 8 >= left) v2 = none;
+              if (2 * t + 9 >= left) v3 = none;
+            }
+          }
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             // words hf (dims 16g + 4hf + 0..3) and 2 + hf (dims 16g + 8 + 4hf + 0..3)
@@ -543,19 +681,19 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
               const uint32_t xa = prmt(r0a, r1a, sel), xb = prmt(r0b, r1b, sel);
               const uint32_t ya = prmt(r2a, r3a, sel), yb = prmt(r2b, r3b, sel);
               {
-                const uint32_t av[4] = {bytes_sub(xa, 0x4140u), bytes_sub(xb, 0x4140u),
-                                        bytes_sub(ya, 0x4140u), bytes_sub(yb, 0x4140u)};
+                const uint32_t av[4] = {codes_lo<KV>(xa), codes_lo<KV>(xb), codes_lo<KV>(ya),
+                                        codes_lo<KV>(yb)};
                 mma16816<false>(o[4 * hf + 2 * pp], av, bp);
               }
               {
-                const uint32_t av[4] = {bytes_sub(xa, 0x4342u), bytes_sub(xb, 0x4342u),
-                                        bytes_sub(ya, 0x4342u), bytes_sub(yb, 0x4342u)};
+                const uint32_t av[4] = {codes_hi<KV>(xa), codes_hi<KV>(xb), codes_hi<KV>(ya),
+                                        codes_hi<KV>(yb)};
                 mma16816<false>(o[4 * hf + 2 * pp + 1], av, bp);
               }
             }
           }
         }
-        {
+        if constexpr (!kF8Pool) {
           const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
           mma16816<false>(R, ones, bp);
         }
@@ -607,7 +745,7 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
   }
 }
 
-template <int KV, bool TAIL>
+template <int KV, bool QBF, bool TAIL>
 __global__ void __launch_bounds__(kMaxCtaHeads * 32, 2)
     decode_gqa_kernel(const __grid_constant__ DecodeArgs a) {
   extern __shared__ __align__(1024) unsigned char dsmem[];
@@ -616,40 +754,40 @@ __global__ void __launch_bounds__(kMaxCtaHeads * 32, 2)
   __shared__ int32_t chunk_s;
   // the combine kernel may be scheduled now; it waits for this grid to finish
   asm volatile("griddepcontrol.launch_dependents;");
-  gqa_body<KV, TAIL>(a, dsmem, warp_sum, &abort_s, &chunk_s, blockIdx.x, gridDim.x);
+  gqa_body<KV, QBF, TAIL>(a, dsmem, warp_sum, &abort_s, &chunk_s, blockIdx.x, gridDim.x);
 }
 
-template <int KV, bool TAIL>
+template <int KV, bool QBF, bool TAIL>
 cudaError_t launch_gqa_t(const DecodeArgs& a, int grid, cudaStream_t s) {
   thread_local int opted_in_device = -1;  // per host thread: no shared state
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (opted_in_device != dev) {
-    e = cudaFuncSetAttribute(decode_gqa_kernel<KV, TAIL>,
+    e = cudaFuncSetAttribute(decode_gqa_kernel<KV, QBF, TAIL>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(gqa_smem_bytes<KV>(kMaxBatch, kMaxCtaHeads)));
     if (e != cudaSuccess) return e;
     opted_in_device = dev;
   }
-  decode_gqa_kernel<KV, TAIL>
+  decode_gqa_kernel<KV, QBF, TAIL>
       <<<grid, a.cta_heads * 32, gqa_smem_bytes<KV>(a.batch, a.cta_heads), s>>>(a);
   return cudaGetLastError();
 }
 
-template <int KV, bool TAIL>
+template <int KV, bool QBF, bool TAIL>
 int gqa_occupancy_t(int batch, int w) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   thread_local int cached_dev = -1, cached_batch = -1, cached_w = -1, cached_n = 0;
   if (dev == cached_dev && batch == cached_batch && w == cached_w) return cached_n;
-  if (cudaFuncSetAttribute(decode_gqa_kernel<KV, TAIL>,
+  if (cudaFuncSetAttribute(decode_gqa_kernel<KV, QBF, TAIL>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(gqa_smem_bytes<KV>(kMaxBatch, kMaxCtaHeads))) !=
       cudaSuccess)
     return 0;
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_gqa_kernel<KV, TAIL>, w * 32,
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_gqa_kernel<KV, QBF, TAIL>, w * 32,
                                                     gqa_smem_bytes<KV>(batch, w)) != cudaSuccess)
     return 0;
   cached_dev = dev;
@@ -657,6 +795,36 @@ int gqa_occupancy_t(int batch, int w) {
   cached_w = w;
   cached_n = n;
   return n;
+}
+
+struct GqaLaunch {
+  const DecodeArgs& a;
+  int grid;
+  cudaStream_t s;
+  template <int KV, bool QBF, bool TAIL>
+  cudaError_t run() const { return launch_gqa_t<KV, QBF, TAIL>(a, grid, s); }
+  cudaError_t fail() const { return cudaErrorInvalidValue; }
+};
+
+struct GqaOccupancy {
+  int batch, w;
+  template <int KV, bool QBF, bool TAIL>
+  int run() const { return gqa_occupancy_t<KV, QBF, TAIL>(batch, w); }
+  int fail() const { return 0; }
+};
+
+// f.run<KV, QBF, TAIL>() for the runtime kinds.
+template <typename F>
+auto with_kinds(int kv_dtype, int q_dtype, bool tail, const F& f) -> decltype(f.fail()) {
+  switch (kv_dtype) {
+    case kI8: return tail ? f.template run<kI8, false, true>() : f.template run<kI8, false, false>();
+    case kI4: return tail ? f.template run<kI4, false, true>() : f.template run<kI4, false, false>();
+    case kF8:
+      if (q_dtype == kBF16)
+        return tail ? f.template run<kF8, true, true>() : f.template run<kF8, true, false>();
+      return tail ? f.template run<kF8, false, true>() : f.template run<kF8, false, false>();
+    default: return f.fail();
+  }
 }
 
 }  // namespace
@@ -667,25 +835,17 @@ int decode_gqa_cta_heads(int kv_heads) {
 }
 
 bool decode_gqa_supported(int kv_dtype, int q_dtype, int group, int kv_heads) {
-  return (kv_dtype == kI8 || kv_dtype == kI4) && q_dtype == kF16 && group == kGqaGroup &&
-         decode_gqa_cta_heads(kv_heads) > 0;
+  return (kv_dtype == kF8 || ((kv_dtype == kI8 || kv_dtype == kI4) && q_dtype == kF16)) &&
+         group == kGqaGroup && decode_gqa_cta_heads(kv_heads) > 0;
 }
 
-cudaError_t launch_decode_gqa(const DecodeArgs& a, int kv_dtype, int grid, cudaStream_t s) {
-  const bool tail = a.tail_ctr != nullptr;
-  if (kv_dtype == kI8)
-    return tail ? launch_gqa_t<kI8, true>(a, grid, s) : launch_gqa_t<kI8, false>(a, grid, s);
-  if (kv_dtype == kI4)
-    return tail ? launch_gqa_t<kI4, true>(a, grid, s) : launch_gqa_t<kI4, false>(a, grid, s);
-  return cudaErrorInvalidValue;
+cudaError_t launch_decode_gqa(const DecodeArgs& a, int kv_dtype, int q_dtype, int grid,
+                              cudaStream_t s) {
+  return with_kinds(kv_dtype, q_dtype, a.tail_ctr != nullptr, GqaLaunch{a, grid, s});
 }
 
-int decode_gqa_ctas_per_sm(int kv_dtype, int batch, int w, bool tail) {
-  if (kv_dtype == kI8)
-    return tail ? gqa_occupancy_t<kI8, true>(batch, w) : gqa_occupancy_t<kI8, false>(batch, w);
-  if (kv_dtype == kI4)
-    return tail ? gqa_occupancy_t<kI4, true>(batch, w) : gqa_occupancy_t<kI4, false>(batch, w);
-  return 0;
+int decode_gqa_ctas_per_sm(int kv_dtype, int q_dtype, int batch, int w, bool tail) {
+  return with_kinds(kv_dtype, q_dtype, tail, GqaOccupancy{batch, w});
 }
 
 }  // namespace kvq

@@ -231,8 +231,9 @@ int decode_ctas_per_sm(int kv_dtype, int q_dtype, int batch, bool tail);
 // (encode_pool_map_heads).
 bool decode_gqa_supported(int kv_dtype, int q_dtype, int group, int kv_heads);
 int decode_gqa_cta_heads(int kv_heads);  // kv heads per CTA (0: unsupported)
-cudaError_t launch_decode_gqa(const DecodeArgs& a, int kv_dtype, int grid, cudaStream_t s);
-int decode_gqa_ctas_per_sm(int kv_dtype, int batch, int cta_heads, bool tail);
+cudaError_t launch_decode_gqa(const DecodeArgs& a, int kv_dtype, int q_dtype, int grid,
+                              cudaStream_t s);
+int decode_gqa_ctas_per_sm(int kv_dtype, int q_dtype, int batch, int cta_heads, bool tail);
 // the same for the shared-prefix kernel and a number of groups
 int prefix_ctas_per_sm(int kv_dtype, int q_dtype, int num_groups);
 

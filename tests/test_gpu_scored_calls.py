@@ -107,6 +107,31 @@ def test_random_calls(gpu, seed):
         assert torch.equal(call(), got)  # the same inputs give the same bits
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hkv", [1, 2, 5, 8, 12, 16])
+def test_decode_groups_of_four(gpu, hkv, dtype):
+    """4 q heads per kv head, any number of kv heads; V's scales far apart,
+    blocks of zeros that hold NaN codes, windows of block ids that end inside
+    a request, ids outside the pool."""
+    for lens in ([0, 1, 15, 16, 17, 300, 513, 1100], [2500], [9001, 0, 40]):
+        pool, bt = base.make_pool("fp8", lens, hkv, 60 + hkv, dtype, v_spread=dtype == "bf16")
+        for name in ("k", "v"):
+            at = int(bt[int(np.argmax(lens)), 3])
+            getattr(pool, name + "_sz")[at, hkv - 1] = 0
+            getattr(pool, name)[at, :, hkv - 1] = 0x7F
+        q = base.randn(61, len(lens), 4 * hkv, 128, dtype=dtype)
+        call = Call(pool, q, bt, lens)
+        got = call().clone()
+        call.check()
+        base.compare(pool, got, q, bt, lens)
+        assert torch.equal(call(), got)
+        bad = bt.copy()
+        bad[int(np.argmax(lens)), 2] = pool.num_blocks
+        call.bt = i32(bad)
+        assert torch.isfinite(call()).all()
+        assert int(call.err.item()) == kvq.DEV_ERR_BITS["block_id"]
+
+
 @pytest.mark.parametrize("form", ["decode", "extend"])
 def test_two_calls_at_once(gpu, form):
     """Two calls on two streams, each with its workspace, over one pool."""
