@@ -245,9 +245,9 @@ kvq_status decode_impl(const kvq_pool* pool, const void* q, int32_t q_dtype, voi
   if (!aligned16(out)) return KVQ_ERR_INVALID_ARG;
   kvq::DecodeArgs a;
   std::memset(&a, 0, sizeof(a));
-  // the grouped-query kernel (INT8 / INT4 pools with fp16 queries, FP8 pools; 4
-  // q heads per kv head) serves the plain decode; the fused step keeps the general kernel
-  // the kernels with scores and those over FP8 pools are their own
+  // the grouped-query kernel (INT8 / INT4 pools with fp16 queries and 4 q heads
+  // per kv head, FP8 pools with 2 to 8) serves the plain decode; the fused step
+  // keeps the general kernel; the kernels with scores are their own
   const bool scored = score != nullptr && (score->softcap > 0.f || score->window > 0 ||
                                            score->alibi_slopes != nullptr);
   // FP8 and scored: short contexts, few enough for a warp each: a request is not
@@ -326,7 +326,9 @@ kvq_status decode_impl(const kvq_pool* pool, const void* q, int32_t q_dtype, voi
   if (gqa) {
     // a CTA per group of cta_heads kv heads, one range each; at most
     // kMaxCtasPerSm * 4 warps per SM, as the workspace's records assume
-    const int occ = kvq::decode_gqa_ctas_per_sm(pool->kv_dtype, q_dtype, batch, cta_heads, false);
+    const int occ = kvq::decode_gqa_ctas_per_sm(pool->kv_dtype, q_dtype,
+                                                q_heads / pool->kv_heads, batch, cta_heads,
+                                                false);
     const int per_sm =
         std::min(occ, kvq::kMaxCtasPerSm * (kvq::kDecodeThreads / 32) / cta_heads);
     if (per_sm <= 0) return KVQ_ERR_CUDA;

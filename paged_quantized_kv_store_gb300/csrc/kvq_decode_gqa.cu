@@ -1,6 +1,6 @@
-// kvq_decode_gqa: single-token decode attention with 4 q heads per kv head
-// (grouped-query attention) over INT8 / INT4 pools for queries in fp16, and
-// over FP8 pools for queries in fp16 or bf16.
+// kvq_decode_gqa: single-token decode attention of grouped queries: 4 q heads
+// per kv head over INT8 / INT4 pools for queries in fp16, and 2 to 8 over FP8
+// pools for queries in fp16 or bf16.
 //
 // LMDeploy article (devpress.csdn.net) §2.4: INT8/INT4 KV with a per-token,
 // per-head (scale, zero); §2.2: 16-token blocks reached through block tables;
@@ -70,10 +70,15 @@
 // travel with the stage's position. K's scale multiplies the scores; V's enters
 // P' as 2^(scale - reference), and o is moved to another reference where a
 // block's scale leaves [-2, 7] powers of two of it (P' stays below 2^15). bf16
-// queries enter as fp16 times a power of two for each head (q_to_f16). us
-// against the general kernel, which stages one kv head's tile a copy:
-// 256 x 256-2048, 32/8 heads 110 and 120; 64 x 4096 96 and 103.
+// queries enter as fp16 times a power of two for each head (q_to_f16). Up to 4
+// heads use the duplicated columns (G = 4; columns of no head repeat head 0),
+// 5 to 8 the plain layout (G = 8). us here and in the general kernel, which
+// stages one kv head's tile a copy (8 kv heads): 256 x 256-2048 with 4 q heads
+// per kv head 110 and 120; 64 x 4096 with 2, 4 and 8 92 and 100, 96 and 103, 100
+// and 106; 2 x 90001-131071 with 8 87 and 93; 16 x 500 with 4 14.3 and 13.7.
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "kvq_decode_common.cuh"
 #include "kvq_device.cuh"
@@ -84,7 +89,6 @@
 namespace kvq {
 namespace {
 
-constexpr int kGqaGroup = 4;              // q heads per kv head served by this kernel
 constexpr int kMaxCtaHeads = 8;           // warps (kv heads) per CTA
 constexpr uint32_t kLoNib = 0x000F000Fu;  // nibble at bits 0-3 of each half: c
 constexpr uint32_t kHiNib = 0x00F000F0u;  // nibble at bits 4-7 of each half: 16 c
@@ -177,13 +181,14 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity
   return true;
 }
 
-template <int KV, bool QBF, bool TAIL>
+template <int KV, bool QBF, bool TAIL, int G>
 __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsmem,
                                          int32_t* warp_sum, volatile int* abort_s,
                                          int32_t* chunk_s, int cta, int ncta) {
   using S = CtaStage<KV>;
   constexpr int D = S::kDepth;
   constexpr bool kF8Pool = KV == kF8;
+  static_assert(G == 4 || (G == 8 && kF8Pool), "q heads a warp holds");
   constexpr float kMid = KV == kI8 ? 128.f : 8.f;
   constexpr bool kLockstep = KV != kI4;
 
@@ -192,7 +197,12 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
   const int g = lane >> 2, t = lane & 3;
   const int tsel = t >> 1;       // 0: this lane scores token g, 1: token g + 8
   const int hp = t & 1;          // ... for q heads 2 hp and 2 hp + 1 of the group
-  const int tau = g + 8 * tsel;  // that token's row in the block
+  // G = 8: columns 0-7 are the (up to 8) heads, a lane scores tokens g and g + 8
+  // for heads 2t, 2t + 1, and nothing is duplicated
+  constexpr bool kDup = G == 4;
+  constexpr int kTok = kDup ? 1 : 2;  // tokens a lane scores
+  constexpr int kHeadLanes = kDup ? 2 : 4;  // the lanes from this distance on hold the same heads
+  const int tau = g + (kDup ? 8 * tsel : 0);  // the (first) token's row in the block
   const bool producer = warp == 0;
 
   const StreamPlan sp = plan_stream<QBF, TAIL>(a, dsmem, warp_sum, cta, ncta, kLockstep,
@@ -358,7 +368,8 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
     // ---- per-request state of this warp's kv head -------------------------------------
     uint32_t seg_key = 0xFFFFFFFFu;
     int L = 0, seg_nblk = 0, seg_skip = 0, hq0 = 0, seg_b = 0;
-    const int hh0 = warp * kGqaGroup;  // this warp's first record row in the group
+    const int group = a.group;   // at most G (INT8, INT4: G)
+    const int hh0 = warp * group;  // this warp's first record row in the group
     int64_t seg_start = 0;
     uint32_t qb[8][2];           // Q as the B operand of S^T = K Q^T (dims permuted like K)
     // sm_scale log2(e) sum(q) of this lane's two heads; FP8 pools: the factors that
@@ -375,24 +386,27 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
       // the lanes of heads (2 hp, 2 hp + 1): t and t ^ 2, every g; columns 2t + u
       // and 2t + u + 4 hold the two token halves of head 2 hp + u
 #pragma unroll
-      for (int off = 2; off < 32; off <<= 1) {
+      for (int off = kHeadLanes; off < 32; off <<= 1) {
         l0 += __shfl_xor_sync(kFull, l0, off);
         l1 += __shfl_xor_sync(kFull, l1, off);
         z0 += __shfl_xor_sync(kFull, z0, off);
         z1 += __shfl_xor_sync(kFull, z1, off);
       }
+      if constexpr (kDup) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) o[i][c] += __shfl_xor_sync(kFull, o[i][c], 2);
-      R[0] += __shfl_xor_sync(kFull, R[0], 2);
-      R[1] += __shfl_xor_sync(kFull, R[1], 2);
-      if (tsel != 0) return;  // lanes t = 2, 3 now hold copies
+          for (int c = 0; c < 4; ++c) o[i][c] += __shfl_xor_sync(kFull, o[i][c], 2);
+        R[0] += __shfl_xor_sync(kFull, R[0], 2);
+        R[1] += __shfl_xor_sync(kFull, R[1], 2);
+        if (tsel != 0) return;  // lanes t = 2, 3 now hold copies
+      }
       const bool contained = seg_start >= x0 && seg_start + seg_nblk <= x0 + n;
       const int64_t row0 = static_cast<int64_t>(seg_b) * a.q_heads + hq0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int hh = 2 * t + u;
+        if (kF8Pool && hh >= group) continue;
         const float l = u ? l1 : l0, m = u ? m1 : m0;
         const float corr = kF8Pool ? 0.f : (u ? z1 : z0) - kMid * R[u];
         float acc[16];
@@ -459,12 +473,14 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
         seg_nblk = cum[seg_b + 1] - cum[seg_b];
         L = lown[seg_b];
         seg_skip = skip_of(a, seg_b);
-        hq0 = (hgi * W + warp) * kGqaGroup;
-        // Q of head hq0 + (g mod 4) (columns 4-7 repeat 0-3), dims [32t, 32t + 32)
+        hq0 = (hgi * W + warp) * group;
+        // Q of head hq0 + (g mod G) (G = 4: columns 4-7 repeat 0-3; columns of no
+        // head repeat head 0), dims [32t, 32t + 32)
+        const int col = kF8Pool && (g & (G - 1)) >= group ? 0 : g & (G - 1);
         uint32_t qw[16];
         const uint4* qp = reinterpret_cast<const uint4*>(
             static_cast<const uint16_t*>(a.q) +
-            (static_cast<int64_t>(seg_b) * a.q_heads + hq0 + (g & 3)) * kHeadDim + 32 * t);
+            (static_cast<int64_t>(seg_b) * a.q_heads + hq0 + col) * kHeadDim + 32 * t);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint4 v = qp[i];
@@ -490,8 +506,9 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
           }
         }
         if constexpr (kF8Pool) {
-          qz0 = lsc * __shfl_sync(kFull, down, (2 * hp) * 4);  // lanes 4h hold head h
-          qz1 = lsc * __shfl_sync(kFull, down, (2 * hp + 1) * 4);
+          const int h0 = kDup ? 2 * hp : 2 * t;  // lanes 4h hold head h
+          qz0 = lsc * __shfl_sync(kFull, down, h0 * 4);
+          qz1 = lsc * __shfl_sync(kFull, down, (h0 + 1) * 4);
           vref = 0u;
         } else {
           float part = 0.f;
@@ -554,26 +571,41 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
         const float d1a = KV == kI4 ? fmaf(sb[1], 1.f / 16.f, sa[1]) : sa[1] + sb[1];
         const float d0b = KV == kI4 ? fmaf(sb[2], 1.f / 16.f, sa[2]) : sa[2] + sb[2];
         const float d1b = KV == kI4 ? fmaf(sb[3], 1.f / 16.f, sa[3]) : sa[3] + sb[3];
-        const float d0 = tsel ? d0b : d0a, d1 = tsel ? d1b : d1a;
-        float s0, s1;
+        // s[k][u]: the lane's token k, its head u
+        float s[kTok][2];
         if constexpr (kF8Pool) {
-          const float sk = fp8_scale(ksz);
-          s0 = ksz != 0u ? d0 * (sk * qz0) : 0.f;
-          s1 = ksz != 0u ? d1 * (sk * qz1) : 0.f;
+          const float sk0 = fp8_scale(ksz) * qz0, sk1 = fp8_scale(ksz) * qz1;
+          const float dk[2][2] = {{d0a, d1a}, {d0b, d1b}};
+#pragma unroll
+          for (int k = 0; k < kTok; ++k) {
+            const float d0 = kDup && tsel ? dk[1][0] : dk[k][0];
+            const float d1 = kDup && tsel ? dk[1][1] : dk[k][1];
+            s[k][0] = ksz != 0u ? d0 * sk0 : 0.f;
+            s[k][1] = ksz != 0u ? d1 * sk1 : 0.f;
+          }
         } else {
+          const float d0 = tsel ? d0b : d0a, d1 = tsel ? d1b : d1a;
           const float sk = half_lo(ksz) * (kTwo24 * lsc), zk = half_hi(ksz);
-          s0 = fmaf(sk, d0, zk * qz0);
-          s1 = fmaf(sk, d1, zk * qz1);
+          s[0][0] = fmaf(sk, d0, zk * qz0);
+          s[0][1] = fmaf(sk, d1, zk * qz1);
         }
-        if ((j + 1) * kBlock > L && j * kBlock + tau >= L) s0 = s1 = -INFINITY;
+        if ((j + 1) * kBlock > L) {
+#pragma unroll
+          for (int k = 0; k < kTok; ++k)
+            if (j * kBlock + tau + 8 * k >= L) s[k][0] = s[k][1] = -INFINITY;
+        }
+        float bm0 = s[0][0], bm1 = s[0][1];
+        if constexpr (!kDup) {
+          bm0 = fmaxf(bm0, s[kTok - 1][0]);
+          bm1 = fmaxf(bm1, s[kTok - 1][1]);
+        }
         const float sv = kF8Pool ? 1.f : half_lo(vsz);
         // ---- online softmax: the running maximum moves when a score passes it by
         // more than the slack (by anything, for a token with a large V scale) ------
         const float slack = sv <= kSlackMaxScale ? kSlack : 0.f;
-        if (__any_sync(kFull, s0 > m0 + slack || s1 > m1 + slack)) {
-          float bm0 = s0, bm1 = s1;
+        if (__any_sync(kFull, bm0 > m0 + slack || bm1 > m1 + slack)) {
 #pragma unroll
-          for (int off = 2; off < 32; off <<= 1) {
+          for (int off = kHeadLanes; off < 32; off <<= 1) {
             bm0 = fmaxf(bm0, __shfl_xor_sync(kFull, bm0, off));
             bm1 = fmaxf(bm1, __shfl_xor_sync(kFull, bm1, off));
           }
@@ -589,9 +621,14 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
           m0 = mn0;
           m1 = mn1;
         }
-        const float p0 = ex2(s0 - m0), p1 = ex2(s1 - m1);
-        l0 += p0;
-        l1 += p1;
+        float p[kTok][2];
+#pragma unroll
+        for (int k = 0; k < kTok; ++k) {
+          p[k][0] = ex2(s[k][0] - m0);
+          p[k][1] = ex2(s[k][1] - m1);
+          l0 += p[k][0];
+          l1 += p[k][1];
+        }
         float pv = sv;  // what turns p into P'
         if constexpr (kF8Pool) {
           if (vsz != 0u) {
@@ -614,15 +651,21 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
           }
         } else {
           const float zm = fmaf(kMid, sv, half_hi(vsz));
-          z0 = fmaf(p0, zm, z0);
-          z1 = fmaf(p1, zm, z1);
+          z0 = fmaf(p[0][0], zm, z0);
+          z1 = fmaf(p[0][1], zm, z1);
         }
         // P'^T as the B operand: tokens 0-7 into columns 0-3 (lanes t = 0, 1),
         // tokens 8-15 into columns 4-7 (lanes t = 2, 3); the rest zero
-        const uint32_t hpk = pack2<false>(p0 * pv, p1 * pv);
+        // (G = 8: tokens 0-7 and 8-15 into the two halves of the k dimension)
         uint32_t bp[2];
-        bp[0] = movmatrix_trans(tsel ? 0u : hpk);
-        bp[1] = movmatrix_trans(tsel ? hpk : 0u);
+        const uint32_t hpk = pack2<false>(p[0][0] * pv, p[0][1] * pv);
+        if constexpr (kDup) {
+          bp[0] = movmatrix_trans(tsel ? 0u : hpk);
+          bp[1] = movmatrix_trans(tsel ? hpk : 0u);
+        } else {
+          bp[0] = movmatrix_trans(hpk);
+          bp[1] = movmatrix_trans(pack2<false>(p[kTok - 1][0] * pv, p[kTok - 1][1] * pv));
+        }
         // ---- O^T += V^T P'^T over 8 tiles of 16 dims, and sum(P') ---------------------
         if constexpr (KV == kI4) {
           const uint2 v0 = lds64(st + vro[0]), v1 = lds64(st + vro[1]);  // rows 2t, 2t+1
@@ -745,7 +788,7 @@ __device__ __forceinline__ void gqa_body(const DecodeArgs& a, unsigned char* dsm
   }
 }
 
-template <int KV, bool QBF, bool TAIL>
+template <int KV, bool QBF, bool TAIL, int G>
 __global__ void __launch_bounds__(kMaxCtaHeads * 32, 2)
     decode_gqa_kernel(const __grid_constant__ DecodeArgs a) {
   extern __shared__ __align__(1024) unsigned char dsmem[];
@@ -754,40 +797,40 @@ __global__ void __launch_bounds__(kMaxCtaHeads * 32, 2)
   __shared__ int32_t chunk_s;
   // the combine kernel may be scheduled now; it waits for this grid to finish
   asm volatile("griddepcontrol.launch_dependents;");
-  gqa_body<KV, QBF, TAIL>(a, dsmem, warp_sum, &abort_s, &chunk_s, blockIdx.x, gridDim.x);
+  gqa_body<KV, QBF, TAIL, G>(a, dsmem, warp_sum, &abort_s, &chunk_s, blockIdx.x, gridDim.x);
 }
 
-template <int KV, bool QBF, bool TAIL>
+template <int KV, bool QBF, bool TAIL, int G>
 cudaError_t launch_gqa_t(const DecodeArgs& a, int grid, cudaStream_t s) {
   thread_local int opted_in_device = -1;  // per host thread: no shared state
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (opted_in_device != dev) {
-    e = cudaFuncSetAttribute(decode_gqa_kernel<KV, QBF, TAIL>,
+    e = cudaFuncSetAttribute(decode_gqa_kernel<KV, QBF, TAIL, G>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(gqa_smem_bytes<KV>(kMaxBatch, kMaxCtaHeads)));
     if (e != cudaSuccess) return e;
     opted_in_device = dev;
   }
-  decode_gqa_kernel<KV, QBF, TAIL>
+  decode_gqa_kernel<KV, QBF, TAIL, G>
       <<<grid, a.cta_heads * 32, gqa_smem_bytes<KV>(a.batch, a.cta_heads), s>>>(a);
   return cudaGetLastError();
 }
 
-template <int KV, bool QBF, bool TAIL>
+template <int KV, bool QBF, bool TAIL, int G>
 int gqa_occupancy_t(int batch, int w) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   thread_local int cached_dev = -1, cached_batch = -1, cached_w = -1, cached_n = 0;
   if (dev == cached_dev && batch == cached_batch && w == cached_w) return cached_n;
-  if (cudaFuncSetAttribute(decode_gqa_kernel<KV, QBF, TAIL>,
+  if (cudaFuncSetAttribute(decode_gqa_kernel<KV, QBF, TAIL, G>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(gqa_smem_bytes<KV>(kMaxBatch, kMaxCtaHeads))) !=
       cudaSuccess)
     return 0;
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_gqa_kernel<KV, QBF, TAIL>, w * 32,
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_gqa_kernel<KV, QBF, TAIL, G>, w * 32,
                                                     gqa_smem_bytes<KV>(batch, w)) != cudaSuccess)
     return 0;
   cached_dev = dev;
@@ -801,28 +844,32 @@ struct GqaLaunch {
   const DecodeArgs& a;
   int grid;
   cudaStream_t s;
-  template <int KV, bool QBF, bool TAIL>
-  cudaError_t run() const { return launch_gqa_t<KV, QBF, TAIL>(a, grid, s); }
+  template <int KV, bool QBF, bool TAIL, int G = 4>
+  cudaError_t run() const { return launch_gqa_t<KV, QBF, TAIL, G>(a, grid, s); }
   cudaError_t fail() const { return cudaErrorInvalidValue; }
 };
 
 struct GqaOccupancy {
   int batch, w;
-  template <int KV, bool QBF, bool TAIL>
-  int run() const { return gqa_occupancy_t<KV, QBF, TAIL>(batch, w); }
+  template <int KV, bool QBF, bool TAIL, int G = 4>
+  int run() const { return gqa_occupancy_t<KV, QBF, TAIL, G>(batch, w); }
   int fail() const { return 0; }
 };
 
-// f.run<KV, QBF, TAIL>() for the runtime kinds.
+// f.run<KV, QBF, TAIL, G>() for the runtime kinds.
 template <typename F>
-auto with_kinds(int kv_dtype, int q_dtype, bool tail, const F& f) -> decltype(f.fail()) {
+auto with_kinds(int kv_dtype, int q_dtype, bool tail, int group, const F& f)
+    -> decltype(f.fail()) {
+  auto f8 = [&](auto qbf) {
+    constexpr bool kQbf = decltype(qbf)::value;
+    if (group <= 4)
+      return tail ? f.template run<kF8, kQbf, true>() : f.template run<kF8, kQbf, false>();
+    return tail ? f.template run<kF8, kQbf, true, 8>() : f.template run<kF8, kQbf, false, 8>();
+  };
   switch (kv_dtype) {
     case kI8: return tail ? f.template run<kI8, false, true>() : f.template run<kI8, false, false>();
     case kI4: return tail ? f.template run<kI4, false, true>() : f.template run<kI4, false, false>();
-    case kF8:
-      if (q_dtype == kBF16)
-        return tail ? f.template run<kF8, true, true>() : f.template run<kF8, true, false>();
-      return tail ? f.template run<kF8, false, true>() : f.template run<kF8, false, false>();
+    case kF8: return q_dtype == kBF16 ? f8(std::true_type{}) : f8(std::false_type{});
     default: return f.fail();
   }
 }
@@ -835,17 +882,19 @@ int decode_gqa_cta_heads(int kv_heads) {
 }
 
 bool decode_gqa_supported(int kv_dtype, int q_dtype, int group, int kv_heads) {
-  return (kv_dtype == kF8 || ((kv_dtype == kI8 || kv_dtype == kI4) && q_dtype == kF16)) &&
-         group == kGqaGroup && decode_gqa_cta_heads(kv_heads) > 0;
+  const bool kinds = kv_dtype == kF8 ? group >= 2 && group <= 8
+                                     : (kv_dtype == kI8 || kv_dtype == kI4) && q_dtype == kF16 &&
+                                           group == 4;
+  return kinds && decode_gqa_cta_heads(kv_heads) > 0;
 }
 
 cudaError_t launch_decode_gqa(const DecodeArgs& a, int kv_dtype, int q_dtype, int grid,
                               cudaStream_t s) {
-  return with_kinds(kv_dtype, q_dtype, a.tail_ctr != nullptr, GqaLaunch{a, grid, s});
+  return with_kinds(kv_dtype, q_dtype, a.tail_ctr != nullptr, a.group, GqaLaunch{a, grid, s});
 }
 
-int decode_gqa_ctas_per_sm(int kv_dtype, int q_dtype, int batch, int w, bool tail) {
-  return with_kinds(kv_dtype, q_dtype, tail, GqaOccupancy{batch, w});
+int decode_gqa_ctas_per_sm(int kv_dtype, int q_dtype, int group, int batch, int w, bool tail) {
+  return with_kinds(kv_dtype, q_dtype, tail, group, GqaOccupancy{batch, w});
 }
 
 }  // namespace kvq

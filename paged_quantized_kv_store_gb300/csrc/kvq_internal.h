@@ -225,15 +225,17 @@ int decode_scored_ctas_per_sm(int kv_dtype, int q_dtype, bool scored, int batch)
 // CTAs of the decode kernel resident per SM (occupancy) for a dtype pair and batch
 int decode_ctas_per_sm(int kv_dtype, int q_dtype, int batch, bool tail);
 // The grouped-query decode kernel (kvq_decode_gqa.cu): INT8 / INT4 pools, fp16
-// queries, 4 q heads per kv head, a CTA per group of cta_heads kv heads (one
-// warp each); same workspace and combine, records of cta_heads * 4 q heads.
+// queries, 4 q heads per kv head, and FP8 pools, 2 to 8; a CTA per group of
+// cta_heads kv heads (one warp each); same workspace and combine, records of
+// cta_heads * (q heads per kv head) q heads.
 // Its kh_map / vh_map are the [block][kv head][token][row] views
 // (encode_pool_map_heads).
 bool decode_gqa_supported(int kv_dtype, int q_dtype, int group, int kv_heads);
 int decode_gqa_cta_heads(int kv_heads);  // kv heads per CTA (0: unsupported)
 cudaError_t launch_decode_gqa(const DecodeArgs& a, int kv_dtype, int q_dtype, int grid,
                               cudaStream_t s);
-int decode_gqa_ctas_per_sm(int kv_dtype, int q_dtype, int batch, int cta_heads, bool tail);
+int decode_gqa_ctas_per_sm(int kv_dtype, int q_dtype, int group, int batch, int cta_heads,
+                           bool tail);
 // the same for the shared-prefix kernel and a number of groups
 int prefix_ctas_per_sm(int kv_dtype, int q_dtype, int num_groups);
 

@@ -108,9 +108,10 @@ def test_random_calls(gpu, seed):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("group", [2, 3, 4, 5, 7, 8])
 @pytest.mark.parametrize("hkv", [1, 2, 5, 8, 12, 16])
-def test_decode_groups_of_four(gpu, hkv, dtype):
-    """4 q heads per kv head, any number of kv heads; V's scales far apart,
+def test_decode_groups(gpu, hkv, group, dtype):
+    """2 to 8 q heads per kv head, any number of kv heads; V's scales far apart,
     blocks of zeros that hold NaN codes, windows of block ids that end inside
     a request, ids outside the pool."""
     for lens in ([0, 1, 15, 16, 17, 300, 513, 1100], [2500], [9001, 0, 40]):
@@ -119,7 +120,7 @@ def test_decode_groups_of_four(gpu, hkv, dtype):
             at = int(bt[int(np.argmax(lens)), 3])
             getattr(pool, name + "_sz")[at, hkv - 1] = 0
             getattr(pool, name)[at, :, hkv - 1] = 0x7F
-        q = base.randn(61, len(lens), 4 * hkv, 128, dtype=dtype)
+        q = base.randn(61, len(lens), group * hkv, 128, dtype=dtype)
         call = Call(pool, q, bt, lens)
         got = call().clone()
         call.check()
