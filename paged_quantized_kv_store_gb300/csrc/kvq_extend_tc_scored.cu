@@ -9,15 +9,20 @@
 // block's scale lies within [-8, 7] powers of two of the unit's reference; when
 // a tile's largest scale leaves that range the reference moves to it and O is
 // rescaled in TMEM like for a moved maximum. The row sum's column is not. bf16
-// queries enter as fp16 times a power of two for each row.
+// queries enter as fp16 times a power of two for each row. The producer warp
+// turns a tile's scales into these factors. A 64-token tile of 256 rows takes
+// 1.13 us; left out in turn, the exponentials are 18 of a 4096-token prompt's
+// 154 us (32/8 heads: 893 TFLOP/s), the staging 10, the wait for the last
+// product 9, the maxima 6 and the products 3: the roles are balanced, and the
+// softmax warpgroups' instructions come first.
 //
 // INT8 and INT4 pools with scores keep their codes exact in the products for
 // queries of either type (an fp16 K dequantized once would put an error of
 // 2^-11 sum |q k| into scores that a cap then spreads).
 //
 // Scores: the whole tile of a row goes through the cap and the bias in
-// registers; a tile whose scores are all below 0.6 of the cap takes tanh by its
-// series on the FMA pipe (packed pairs), the others two special-function
+// registers; a tile whose scores are all below 1.25 of the cap takes tanh by a
+// polynomial on the FMA pipe (packed pairs), the others two special-function
 // operations a score. A unit's tiles begin at its first query's window.
 #include <cuda_runtime.h>
 

@@ -133,6 +133,20 @@ def test_decode_groups(gpu, hkv, group, dtype):
         assert int(call.err.item()) == kvq.DEV_ERR_BITS["block_id"]
 
 
+@pytest.mark.parametrize("group,dtype", [(4, "f16"), (8, "bf16")])
+def test_decode_groups_long(gpu, group, dtype):
+    """Shares long enough that their ends are handed out from a counter (over
+    128 blocks for each of two CTAs an SM)."""
+    lens = [110001, 109000, 120007, 112000, 111111, 128016]
+    pool, bt = base.make_pool("fp8", lens, 1, 71, dtype)
+    q = base.randn(72, len(lens), group, 128, dtype=dtype)
+    call = Call(pool, q, bt, lens)
+    for _ in range(2):
+        call()
+        call.check()
+        base.compare(pool, call.out[: len(lens)], q, bt, lens)
+
+
 @pytest.mark.parametrize("form", ["decode", "extend"])
 def test_two_calls_at_once(gpu, form):
     """Two calls on two streams, each with its workspace, over one pool."""
