@@ -724,15 +724,21 @@ static kvq_status extend_impl(const kvq_pool* pool, const kvq_score* score, cons
   // 29 and 34, 43 and 48, with 32 rows 45 and 34, 64 and 47; scored, over a
   // window of 1024, with 48 rows 41 and 48, 64 and 50, with 64 rows 45 and 49,
   // 78 and 51; scored INT8 with 48 rows 66 and 61, 95 and 102, with 64 rows 74
-  // and 62, 117 and 101.
+  // and 62, 117 and 101. Short contexts of few rows stay with mma.sync (one request,
+  // FP8): 16 tokens of 16 4 and 9, 64 of 64 7 and 13, 64 of 500 16 and 20; 4 x 50
+  // of 200 18 and 15, 256 of 1000 55 and 29.
   const int group = q_heads / pool->kv_heads;
   const int64_t tc_units = static_cast<int64_t>(pool->kv_heads) *
                            ((static_cast<int64_t>(total_q) * group + 255) / 256);
   const bool tc_pays = fp8 || scored
                            ? static_cast<int64_t>(total_q) * group >= int64_t{kTcPayRows} * batch * (scored ? 2 : 1)
                            : tc_units >= sms;
+  const int64_t units16 = static_cast<int64_t>(pool->kv_heads) *
+                          ((static_cast<int64_t>(total_q) * group +
+                            15 * std::min(batch, total_q)) / 16);
+  const bool small = (fp8 || scored) && units16 <= sms && max_kv_len <= 512;
   const bool use_tc = variant == KVQ_EXTEND_TCGEN05 ||
-                      (variant == KVQ_EXTEND_AUTO && tc_ok && tc_pays);
+                      (variant == KVQ_EXTEND_AUTO && tc_ok && tc_pays && !small);
   const ExtendPlan plan =
       use_tc && (fp8 || scored)
           ? extend_tc_plan(batch, total_q, q_heads, pool->kv_heads, max_kv_len,
@@ -774,12 +780,30 @@ static kvq_status extend_impl(const kvq_pool* pool, const kvq_score* score, cons
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_off);
   a.dev_err = dev_err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(a.counter, 0, sizeof(int32_t), s) != cudaSuccess) return KVQ_ERR_CUDA;
+  int scored_per_sm = 1;
+  if (fp8 || scored) {
+    scored_per_sm =
+        use_tc ? kvq::extend_tc_scored_ctas_per_sm(pool->kv_dtype, q_dtype, scored, batch)
+               : kvq::extend_scored_ctas_per_sm(pool->kv_dtype, q_dtype, scored, batch);
+    if (scored_per_sm <= 0) return KVQ_ERR_CUDA;
+    // few units: a CTA (tcgen05) or a warp for each, and no counter to zero
+    // (64 tokens over 500, us with the counter and without: mma.sync, whose units
+    // are also spread over the SMs so, 22.6 and 16.3, tcgen05 22.8 and 20.0)
+    const int rows = use_tc ? 256 : 16;
+    const int64_t units =
+        pool->kv_heads *
+        ((static_cast<int64_t>(total_q) * group + (rows - 1) * std::min(batch, total_q)) / rows) *
+        plan.max_splits;
+    const int64_t workers =
+        use_tc ? sms : static_cast<int64_t>(sms) * scored_per_sm * (kvq::kDecodeThreads / 32);
+    if (units <= workers) a.counter = nullptr;
+  }
+  if (a.counter != nullptr &&
+      cudaMemsetAsync(a.counter, 0, sizeof(int32_t), s) != cudaSuccess)
+    return KVQ_ERR_CUDA;
   if (use_tc) {
     // persistent CTAs, one per SM (each holds all 512 TMEM columns)
     if (fp8 || scored) {
-      if (kvq::extend_tc_scored_ctas_per_sm(pool->kv_dtype, q_dtype, scored, batch) <= 0)
-        return KVQ_ERR_CUDA;
       return kvq::launch_extend_tc_scored(a, pool->kv_dtype, q_dtype, scored, sms, s) ==
                      cudaSuccess
                  ? KVQ_OK
@@ -791,9 +815,7 @@ static kvq_status extend_impl(const kvq_pool* pool, const kvq_score* score, cons
                : KVQ_ERR_CUDA;
   }
   if (fp8 || scored) {
-    const int n = kvq::extend_scored_ctas_per_sm(pool->kv_dtype, q_dtype, scored, batch);
-    if (n <= 0) return KVQ_ERR_CUDA;
-    return kvq::launch_extend_scored(a, pool->kv_dtype, q_dtype, scored, sms * n, s) ==
+    return kvq::launch_extend_scored(a, pool->kv_dtype, q_dtype, scored, sms * scored_per_sm, s) ==
                    cudaSuccess
                ? KVQ_OK
                : KVQ_ERR_CUDA;

@@ -162,10 +162,14 @@ __global__ void __launch_bounds__(kDecodeThreads)
   }
   uint32_t phase = 0;  // parity to wait for, per stage (TMA path)
 
-  for (;;) {
+  for (int turn = 0;; ++turn) {
     int u = 0;
-    if (lane == 0) u = atomicAdd(a.counter, 1);
-    u = __shfl_sync(kFull, u, 0);
+    if ((KV == kF8 || SC) && a.counter == nullptr) {  // every warp has at most one unit
+      u = turn == 0 ? static_cast<int>(warp * gridDim.x + blockIdx.x) : total;
+    } else {
+      if (lane == 0) u = atomicAdd(a.counter, 1);
+      u = __shfl_sync(kFull, u, 0);
+    }
     if (u >= total) break;
     int lo = 0, hi = a.batch - 1;  // largest b with ucum[b] <= u: a request with work
     while (lo < hi) {

@@ -939,7 +939,7 @@ struct TcShared {
 
 // ---- roles ------------------------------------------------------------------------
 
-// Hands out unit k (an atomic counter) through slot k mod 2 once every
+// Hands out unit k (from an atomic counter) through slot k mod 2 once every
 // working warp has read unit k - 2 from it, with what the roles want to know of
 // it: looking the request up costs a chain of loads that one thread, running
 // ahead, takes for all. That thread is the raw-ring producer's lane 0 (INT8 and
@@ -948,7 +948,10 @@ struct TcShared {
 template <bool SC, bool SPLIT>
 __device__ __forceinline__ void publish_unit(const ExtendArgs& a, const TcShared& c, uint32_t k) {
   const uint32_t slot = k & 1u;
-  const int u = atomicAdd(a.counter, 1);
+  // (no counter: every CTA has at most one unit, its own)
+  const int u = !SPLIT || a.counter != nullptr ? atomicAdd(a.counter, 1)
+                : k == 0                       ? static_cast<int>(blockIdx.x)
+                                               : c.total;
   TcUnit w;
   w.live = u < c.total;
   if (w.live) w = tc_unit<SC, SPLIT>(a, c.ucum, u);

@@ -159,7 +159,7 @@ struct ExtendArgs {
   int max_splits;              // records per (query row, q head) when split
   int len_cap;                 // longest context accepted (tokens)
   float sm_scale_log2;
-  int32_t* counter;            // work counter (zero at launch)
+  int32_t* counter;            // work counter (zero at launch); null: at most a unit a worker
   float* part;                 // [total_q][Hq][max_splits][kPartStride] when split
   int32_t* dev_err;
   const uint8_t* k_se;         // FP8 pools: the scale bytes [num_blocks][kv_heads]
